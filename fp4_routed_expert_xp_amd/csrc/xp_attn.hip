@@ -1,0 +1,706 @@
+// xp_attn.hip — attention of a few query rows per sequence over the 4-bit cache.
+//
+// For each sequence and kv head, row r (query token r / group, head r % group of
+// the kv head's group) holds softmax(scale * q . k) over the positions it sees,
+// times v, in one pass over the cache with a running maximum and sum.
+//
+// One wave takes 64 positions at a time. Scores are formed transposed,
+// S^T = K Q^T (v_mfma_f32_16x16x32_f16, K's positions as the rows), which leaves
+// lane (c, q) = (lane % 16, lane / 16) with query row c at positions
+// 16 t + 4 q + i (t, i = 0..3): the exponentials, once rounded to fp16, are then
+// already the operand of O^T += V^T P^T with no movement between lanes, since the
+// order of positions inside a contraction is free as long as V follows it. V's
+// codes pass through LDS for that: a 4-bit transposing read hands each lane 16
+// positions of one of V's columns in just that order.
+//
+// Precision: codes times scales are exact in fp16 (six significant bits). q in
+// bf16 is scaled by a power of two to fp16, row by row, which is exact for every
+// value within 2^28 of its row's largest. Scores, maxima, sums and outputs are
+// fp32. Exponentials round once to fp16 (2^-11), held as 2^15 p: what falls below
+// fp16's normal numbers is then within 2^-40 of the row's largest.
+#include "xp_kv_dev.h"
+
+namespace xp {
+namespace attn {
+
+using kv::Geo;
+
+typedef __attribute__((ext_vector_type(2))) _Float16 h16x2;
+typedef __attribute__((ext_vector_type(8))) _Float16 h16x8;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(2))) int i32x2;
+
+constexpr int kWaves = 4;
+constexpr float kLift = 15.0f;   // exponentials are held as 2^kLift p: 2^15 is fp16's largest power of two
+
+struct Args {
+    Geo g;
+    const void* q;
+    long long q_stride;
+    const uint8_t* cache;
+    const int32_t* table;
+    const int32_t* lens;
+    void* out;
+    long long out_stride;
+    float* part;          // partial outputs of the splits, unscaled
+    float* part_ml;       // their maxima and sums
+    float* lse;           // per row: the maximum in log2 units and the sum's logarithm, for the weights
+    float* weights;
+    long long w_stride;
+    int heads, group, q_rows, row_blocks, splits, window;
+    float scale_m;        // scale * log2(e) = scale_m * 2^scale_e
+    int scale_e;
+};
+
+__device__ __forceinline__ float max_over_q(float x) {
+    uint32_t u = __float_as_uint(x);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    u = __float_as_uint(x);
+    auto b = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_over_q(float x) {
+    uint32_t u = __float_as_uint(x);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    u = __float_as_uint(x);
+    auto b = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+__device__ __forceinline__ h16x8 frag(h16x2 a, h16x2 b, h16x2 c, h16x2 d) {
+    return h16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Eight e2m1 codes times their scale (two values a pair, or one for all), exact.
+__device__ __forceinline__ h16x8 decode8(uint32_t w, h16x2 s0, h16x2 s1, h16x2 s2, h16x2 s3) {
+    return frag(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s0, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s1,
+                __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s3);
+}
+
+template <int D>
+struct Dim {
+    static constexpr int NG = D / 32;          // groups
+    static constexpr int NW = D / 32;          // dwords of K codes a lane holds of each position: D/8 dwords over 4 lanes
+    static constexpr int NH = D / 16;          // 16-value columns of V
+    static constexpr int VD = D / 8;           // dwords of V codes a lane copies
+    static constexpr int kVBytes = 64 * D / 2; // V codes of a tile
+};
+
+// The 8 dims that dword w of lane quarter q covers.
+template <int D>
+__device__ __forceinline__ int dims_of(int q, int w) {
+    if constexpr (D == 64) return 16 * q + 8 * w;
+    return 128 * (w >> 2) + 32 * q + 8 * (w & 3);
+}
+
+// Query rows of a block of 16*MT as fp16 fragments, and each row's score factor.
+template <int D, int MT, bool BF16>
+__device__ __forceinline__ void load_q(const Args& a, int b, int head, int rb, int c, int q, h16x8 (&qf)[MT][Dim<D>::NW],
+                                       float (&factor)[MT]) {
+    const int rows = a.q_rows * a.group;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int r = (rb * MT + mt) * 16 + c;
+        const bool ok = r < rows;
+        const int tok = ok ? r / a.group : 0;
+        const int hd = head * a.group + (ok ? r - tok * a.group : 0);
+        const uint16_t* p = (const uint16_t*)a.q + ((long long)b * a.q_rows + tok) * a.q_stride + (long long)hd * D;
+        uint4 v[Dim<D>::NW];
+#pragma unroll
+        for (int w = 0; w < Dim<D>::NW; ++w) v[w] = ok ? *(const uint4*)(p + dims_of<D>(q, w)) : uint4{0, 0, 0, 0};
+        int k = 0;
+        if constexpr (BF16) {
+            uint32_t top = 0;                   // exponent field of the row's largest magnitude
+#pragma unroll
+            for (int w = 0; w < Dim<D>::NW; ++w) {
+                const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = (u[i] >> 7) & 255u, hi = (u[i] >> 23) & 255u;
+                    top = lo > top ? lo : top;
+                    top = hi > top ? hi : top;
+                }
+            }
+            const int e = (int)max_over_q((float)top);
+            // largest magnitude to [2^14, 2^15); rows with an infinity or NaN are left as they are
+            k = e == 255 ? 0 : 141 - e;
+            k = k > 100 ? 100 : k;
+            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+#pragma unroll
+            for (int w = 0; w < Dim<D>::NW; ++w) {
+                const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+                h16x8 f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[2 * i] = (_Float16)(__uint_as_float(u[i] << 16) * up);
+                    f[2 * i + 1] = (_Float16)(__uint_as_float(u[i] & 0xffff0000u) * up);
+                }
+                qf[mt][w] = f;
+            }
+        } else {
+#pragma unroll
+            for (int w = 0; w < Dim<D>::NW; ++w) qf[mt][w] = __builtin_bit_cast(h16x8, v[w]);
+        }
+        // kept a normal number: a masked -inf times 0, or a score of 0 times infinity, would be NaN
+        factor[mt] = fminf(fmaxf(__builtin_amdgcn_ldexpf(a.scale_m, a.scale_e - k), 0x1p-126f), 0x1p127f);
+    }
+}
+
+// K codes and scales of a tile as a lane of the score product holds them.
+template <int D>
+struct KTile {
+    uint32_t w[4][Dim<D>::NW];
+    uint32_t s[D == 256 ? 2 : 1];
+};
+template <int D>
+__device__ __forceinline__ void load_k(KTile<D>& k, const uint8_t* t, int c, int q) {
+    constexpr int NG = Dim<D>::NG;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const int pos = 16 * b + c;
+        if constexpr (D == 64) {
+            const uint2 v = *(const uint2*)(t + (q >> 1) * 1024 + pos * 16 + (q & 1) * 8);
+            k.w[b][0] = v.x;
+            k.w[b][1] = v.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < NG / 4; ++j) {
+                const uint4 v = *(const uint4*)(t + (4 * j + q) * 1024 + pos * 16);
+                k.w[b][4 * j] = v.x;
+                k.w[b][4 * j + 1] = v.y;
+                k.w[b][4 * j + 2] = v.z;
+                k.w[b][4 * j + 3] = v.w;
+            }
+        }
+    }
+    if constexpr (D == 64) {
+        k.s[0] = *(const uint32_t*)(t + NG * 1024 + (q >> 1) * 64 + c * 4);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NG / 4; ++j) k.s[j] = *(const uint32_t*)(t + NG * 1024 + (4 * j + q) * 64 + c * 4);
+    }
+}
+// Fragment w of block b: its eight codes times the scale of position 16 b + c.
+template <int D>
+__device__ __forceinline__ h16x8 k_frag(const KTile<D>& k, int b, int w) {
+    const uint32_t sd = k.s[D == 256 ? w >> 2 : 0];
+    const h16x2 p = b < 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sd, 1.0f, false)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sd, 1.0f, true);
+    const _Float16 s = b & 1 ? p.y : p.x;
+    const h16x2 ss = h16x2{s, s};
+    return decode8(k.w[b][w], ss, ss, ss, ss);
+}
+
+// Positions a row sees: from lo (inclusive) to hi (exclusive).
+struct Span {
+    int lo, hi;
+};
+__device__ __forceinline__ Span span_of(const Args& a, int len, int r) {
+    const int rows = a.q_rows * a.group;
+    const int at = len - a.q_rows + r / a.group;          // the row's own position
+    Span s;
+    s.hi = r < rows ? at + 1 : 0;
+    s.lo = a.window > 0 && at - a.window + 1 > 0 ? at - a.window + 1 : 0;
+    return s;
+}
+
+__device__ __forceinline__ int length_of(const Args& a, int b) {
+    const int cap = a.g.max_pages * a.g.page;
+    const int n = a.lens[b];
+    return n < 0 ? 0 : (n > cap ? cap : n);
+}
+
+__device__ __forceinline__ uint16_t to16(float f, bool bf16) {
+    return bf16 ? bf16_rne(f) : __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+
+// One workgroup: a split of one (sequence, kv head, block of 16*MT rows); its four
+// waves take tiles in turn and join in LDS.
+template <int D, int MT, bool BF16>
+__global__ __launch_bounds__(256) void attn_decode_kernel(Args a) {
+    constexpr int NW = Dim<D>::NW, NG = Dim<D>::NG, NH = Dim<D>::NH, VD = Dim<D>::VD;
+    constexpr int kRegion = Dim<D>::kVBytes + NG * 64;     // a wave's V codes and scales
+    constexpr int kJoin = MT * NH * 64 * 16;               // one wave's output, fp32
+    constexpr int kLds = kWaves * kRegion > 2 * kJoin ? kWaves * kRegion : 2 * kJoin;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+    __shared__ float join_ml[2][2][MT * 64];
+
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int head = blockIdx.y % a.g.kv_heads, rb = blockIdx.y / a.g.kv_heads, b = blockIdx.z;
+    const int len = length_of(a, b);
+    const int32_t* tr = a.table + (long long)b * a.g.max_pages;
+
+    h16x8 qf[MT][NW];
+    float factor[MT];
+    load_q<D, MT, BF16>(a, b, head, rb, c, q, qf, factor);
+
+    // this block's tiles: those that its rows see, an even share for each split
+    const int first_row = rb * MT * 16, rows = a.q_rows * a.group;
+    const int last_row = first_row + MT * 16 < rows ? first_row + MT * 16 - 1 : rows - 1;
+    const Span s_first = span_of(a, len, first_row), s_last = span_of(a, len, last_row);
+    const int t_lo = s_first.lo >> 6, t_hi = s_last.hi > 0 ? (s_last.hi + 63) >> 6 : 0;
+    const int n = t_hi > t_lo ? t_hi - t_lo : 0;
+    const int per = (n + a.splits - 1) / a.splits;
+    const int t0 = t_lo + blockIdx.x * per;
+    int t1 = t0 + per;
+    t1 = t1 < t_hi ? t1 : t_hi;
+    // tiles that every row sees whole
+    const int full_lo = s_last.lo, full_hi = s_first.hi;
+
+    f32x4 o[MT][NH];
+    float m[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = -__builtin_inff();
+        l[mt] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) o[mt][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    uint8_t* region = lds + wave * kRegion;
+
+    for (int tile = t0 + wave; tile < t1; tile += kWaves) {
+        const long long at = kv::tile_at(a.g, tr, head, tile * 64);
+        if (at < 0) continue;                              // no such page: its positions are not seen
+        const uint8_t* t = a.cache + at;
+        KTile<D> k;
+        load_k<D>(k, t, c, q);
+        uint32_t vw[VD];
+#pragma unroll
+        for (int j = 0; j < VD / 4; ++j) {
+            const uint4 v = *(const uint4*)(t + NG * 1088 + j * 1024 + lane * 16);
+            vw[4 * j] = v.x;
+            vw[4 * j + 1] = v.y;
+            vw[4 * j + 2] = v.z;
+            vw[4 * j + 3] = v.w;
+        }
+        constexpr int SW = NG * 64 / 4;                    // dwords of V scales
+        uint32_t vs[(SW + 63) / 64];
+#pragma unroll
+        for (int j = 0; j < (SW + 63) / 64; ++j)
+            vs[j] = j * 64 + lane < SW ? *(const uint32_t*)(t + NG * 2112 + (j * 64 + lane) * 4) : 0u;
+
+        f32x4 s[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int bl = 0; bl < 4; ++bl) s[mt][bl] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int bl = 0; bl < 4; ++bl)
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const h16x8 kf = k_frag<D>(k, bl, w);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) s[mt][bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[mt][w], s[mt][bl], 0, 0, 0);
+            }
+
+        const bool masked = tile * 64 < full_lo || tile * 64 + 64 > full_hi;
+        bool nan_v = false;
+        if (masked) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const Span sp = span_of(a, len, (rb * MT + mt) * 16 + c);
+#pragma unroll
+                for (int bl = 0; bl < 4; ++bl)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int pos = tile * 64 + 16 * bl + 4 * q + i;
+                        if (pos < sp.lo || pos >= sp.hi) s[mt][bl][i] = -__builtin_inff();
+                    }
+            }
+            // V where not every row sees it: bytes behind the sequence are no values, and a
+            // NaN scale must not reach rows that do not see its position
+#pragma unroll
+            for (int j = 0; j < (SW + 63) / 64; ++j) {
+                const int at_byte = (j * 64 + lane) * 4;   // byte 4x + y of a group: position 16 (x % 4) + 4 (x / 4) + y
+                const int x = (at_byte & 63) >> 2;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int pos = tile * 64 + 16 * (x & 3) + 4 * (x >> 2) + y;
+                    if (pos >= len) vs[j] &= ~(255u << (8 * y));
+                    if (((vs[j] >> (8 * y)) & 127u) == 127u) nan_v = true;
+                }
+            }
+            nan_v = __ballot(nan_v) != 0;
+        }
+
+        // V to LDS; this wave's earlier reads of the region are done (LDS keeps a wave's order)
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int j = 0; j < VD / 4; ++j)
+            *(uint4*)(region + j * 1024 + lane * 16) = uint4{vw[4 * j], vw[4 * j + 1], vw[4 * j + 2], vw[4 * j + 3]};
+#pragma unroll
+        for (int j = 0; j < (SW + 63) / 64; ++j)
+            if (j * 64 + lane < SW) *(uint32_t*)(region + Dim<D>::kVBytes + (j * 64 + lane) * 4) = vs[j];
+        __builtin_amdgcn_wave_barrier();
+
+        h16x8 p[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float mx = s[mt][0][0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[mt][e >> 2][e & 3]);
+            mx = max_over_q(mx) * factor[mt];
+            if (__ballot(mx > m[mt])) {
+                const float nm = fmaxf(mx, m[mt]);
+                const float safe = nm == -__builtin_inff() ? 0.0f : nm;
+                const float alpha = __builtin_amdgcn_exp2f(m[mt] - safe);
+                m[mt] = nm;
+                l[mt] *= alpha;
+#pragma unroll
+                for (int h = 0; h < NH; ++h) o[mt][h] *= alpha;
+            }
+            const float base = kLift - (m[mt] == -__builtin_inff() ? 0.0f : m[mt]);
+            float add = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][e >> 2][e & 3], factor[mt], base));
+                add += x;
+                p[mt][e >> 3][e & 7] = (_Float16)x;
+            }
+            l[mt] += add;
+        }
+
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const uint4 sc = *(const uint4*)(region + Dim<D>::kVBytes + g * 64 + q * 16);
+            uint32_t sd[4] = {sc.x, sc.y, sc.z, sc.w};
+            bool bad[16];
+            if (masked && nan_v) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t byte = (sd[e >> 2] >> (8 * (e & 3))) & 127u;
+                    bad[e] = byte == 127u;
+                    if (bad[e]) sd[e >> 2] &= ~(255u << (8 * (e & 3)));
+                }
+            }
+            h16x2 sv[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sv[2 * e] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sd[e], 1.0f, false);
+                sv[2 * e + 1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sd[e], 1.0f, true);
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int h = 2 * g + hh;
+                const int pos = 16 * (c >> 2) + 4 * q + (c & 3);
+                const i32x2 vt = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                    (__attribute__((address_space(3))) i32x2*)(region + h * 512 + pos * 8));
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    const h16x8 vf = decode8((uint32_t)vt[st], sv[4 * st], sv[4 * st + 1], sv[4 * st + 2], sv[4 * st + 3]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        o[mt][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[mt][st], o[mt][h], 0, 0, 0);
+                }
+            }
+            if (masked && nan_v) {
+                // rows that see a position whose scale is NaN hold NaN in this group's columns
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const Span sp = span_of(a, len, (rb * MT + mt) * 16 + c);
+                    float hit = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int ps = tile * 64 + 16 * (e >> 2) + 4 * q + (e & 3);
+                        if (bad[e] && ps >= sp.lo && ps < sp.hi) hit = 1.0f;
+                    }
+                    if (max_over_q(hit) > 0.0f) {
+                        o[mt][2 * g] = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+                        o[mt][2 * g + 1] = o[mt][2 * g];
+                    }
+                }
+            }
+        }
+    }
+
+    // join the four waves: 2 and 3 into 0 and 1, then 1 into 0
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) l[mt] = sum_over_q(l[mt]);
+#pragma unroll
+    for (int half = 2; half >= 1; half >>= 1) {
+        __syncthreads();
+        if (wave >= half && wave < 2 * half) {
+            f32x4* buf = (f32x4*)(lds + (wave - half) * kJoin);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) buf[(mt * NH + h) * 64 + lane] = o[mt][h];
+                join_ml[wave - half][0][mt * 64 + lane] = m[mt];
+                join_ml[wave - half][1][mt * 64 + lane] = l[mt];
+            }
+        }
+        __syncthreads();
+        if (wave < half) {
+            const f32x4* buf = (const f32x4*)(lds + wave * kJoin);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const float om = join_ml[wave][0][mt * 64 + lane], ol = join_ml[wave][1][mt * 64 + lane];
+                const float nm = fmaxf(m[mt], om);
+                const float safe = nm == -__builtin_inff() ? 0.0f : nm;
+                const float fa = __builtin_amdgcn_exp2f(m[mt] - safe), fb = __builtin_amdgcn_exp2f(om - safe);
+                m[mt] = nm;
+                l[mt] = l[mt] * fa + ol * fb;
+#pragma unroll
+                for (int h = 0; h < NH; ++h) o[mt][h] = o[mt][h] * fa + buf[(mt * NH + h) * 64 + lane] * fb;
+            }
+        }
+    }
+    if (wave != 0) return;
+
+    const long long blk = ((long long)b * a.g.kv_heads + head) * a.row_blocks + rb;
+    if (a.splits > 1) {
+        f32x4* po = (f32x4*)a.part + (blk * a.splits + blockIdx.x) * (MT * NH * 64);
+        float* pm = a.part_ml + (blk * a.splits + blockIdx.x) * (MT * 32);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) po[(mt * NH + h) * 64 + lane] = o[mt][h];
+            if (q == 0) {
+                pm[mt * 32 + c] = m[mt];
+                pm[mt * 32 + 16 + c] = l[mt];
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int r = (rb * MT + mt) * 16 + c;
+        if (r >= rows) continue;
+        const int tok = r / a.group, hd = head * a.group + r - tok * a.group;
+        uint16_t* y = (uint16_t*)a.out + ((long long)b * a.q_rows + tok) * a.out_stride + (long long)hd * D;
+        const float inv = l[mt] == 0.0f ? 0.0f : 1.0f / l[mt];    // nothing seen: zeros
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            const f32x4 v = o[mt][h] * inv;
+            uint2 w;
+            w.x = (uint32_t)to16(v[0], BF16) | (uint32_t)to16(v[1], BF16) << 16;
+            w.y = (uint32_t)to16(v[2], BF16) | (uint32_t)to16(v[3], BF16) << 16;
+            *(uint2*)(y + 16 * h + 4 * q) = w;
+        }
+        if (a.lse && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
+            l[mt] == 0.0f ? __builtin_inff() : (m[mt] - kLift) + __builtin_amdgcn_logf(l[mt]);
+    }
+}
+
+// Joins the splits in their order: thread = four columns of one row.
+template <int D, int MT, bool BF16>
+__global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
+    constexpr int NH = Dim<D>::NH;
+    const int idx = blockIdx.x * 256 + threadIdx.x;        // (mt, h, lane)
+    if (idx >= MT * NH * 64) return;
+    const int lane = idx & 63, h = (idx >> 6) % NH, mt = (idx >> 6) / NH, c = lane & 15, q = lane >> 4;
+    const int head = blockIdx.y % a.g.kv_heads, rb = blockIdx.y / a.g.kv_heads, b = blockIdx.z;
+    const int r = (rb * MT + mt) * 16 + c;
+    if (r >= a.q_rows * a.group) return;
+    const long long blk = ((long long)b * a.g.kv_heads + head) * a.row_blocks + rb;
+    const f32x4* po = (const f32x4*)a.part + blk * a.splits * (MT * NH * 64) + idx;
+    const float* pm = a.part_ml + blk * a.splits * (MT * 32) + mt * 32 + c;
+    float m = -__builtin_inff();
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, pm[s * MT * 32]);
+    const float safe = m == -__builtin_inff() ? 0.0f : m;
+    f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+    float l = 0.0f;
+    for (int s = 0; s < a.splits; ++s) {
+        const float f = __builtin_amdgcn_exp2f(pm[s * MT * 32] - safe);
+        l = __builtin_fmaf(f, pm[s * MT * 32 + 16], l);
+        o += po[(long long)s * (MT * NH * 64)] * f;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int tok = r / a.group, hd = head * a.group + r - tok * a.group;
+    uint16_t* y = (uint16_t*)a.out + ((long long)b * a.q_rows + tok) * a.out_stride + (long long)hd * D;
+    const f32x4 v = o * inv;
+    uint2 w;
+    w.x = (uint32_t)to16(v[0], BF16) | (uint32_t)to16(v[1], BF16) << 16;
+    w.y = (uint32_t)to16(v[2], BF16) | (uint32_t)to16(v[3], BF16) << 16;
+    *(uint2*)(y + 16 * h + 4 * q) = w;
+    if (a.lse && h == 0 && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
+        l == 0.0f ? __builtin_inff() : (m - kLift) + __builtin_amdgcn_logf(l);
+}
+
+// weights[pos] += the probabilities of all rows of the kv head at pos, from each
+// row's logarithm of the sum. Scores are formed with the rows first (S = Q K^T), so
+// a lane adds four rows of one position by itself and two swaps add the rest; one
+// wave owns a tile, so no atomics. K is read a second time: half the cache's bytes,
+// against writing and reading every row's scores (as much for eight rows a head).
+template <int D, bool BF16>
+__global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
+    constexpr int NW = Dim<D>::NW;
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int head = blockIdx.y, b = blockIdx.z;
+    const int len = length_of(a, b);
+    const int32_t* tr = a.table + (long long)b * a.g.max_pages;
+    const int rows = a.q_rows * a.group;
+    const int t_lo = span_of(a, len, 0).lo >> 6, t_hi = (len + 63) >> 6;
+    const float* lse = a.lse + ((long long)b * a.heads + head * a.group) * a.q_rows;
+    float* weights = a.weights + ((long long)b * a.g.kv_heads + head) * a.w_stride;
+    for (int tile = t_lo + blockIdx.x * kWaves + wave; tile < t_hi; tile += gridDim.x * kWaves) {
+        const long long at = kv::tile_at(a.g, tr, head, tile * 64);
+        if (at < 0) continue;
+        KTile<D> k;
+        load_k<D>(k, a.cache + at, c, q);
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int rb = 0; rb * 16 < rows; ++rb) {
+            h16x8 qf[1][NW];
+            float factor[1];
+            load_q<D, 1, BF16>(a, b, head, rb, c, q, qf, factor);
+            f32x4 s[4];
+#pragma unroll
+            for (int bl = 0; bl < 4; ++bl) {
+                s[bl] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int wd = 0; wd < NW; ++wd)
+                    s[bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[0][wd], k_frag<D>(k, bl, wd), s[bl], 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = rb * 16 + 4 * q + i;
+                const float f = __shfl(factor[0], 4 * q + i);     // held by the lane whose c is the row
+                const float base = r < rows ? -lse[r] : 0.0f;
+                const Span sp = span_of(a, len, r);
+#pragma unroll
+                for (int bl = 0; bl < 4; ++bl) {
+                    const int pos = tile * 64 + 16 * bl + c;
+                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[bl][i], f, base));
+                    w[bl] += pos >= sp.lo && pos < sp.hi ? e : 0.0f;
+                }
+            }
+        }
+        float mine = 0.0f;
+#pragma unroll
+        for (int bl = 0; bl < 4; ++bl) {
+            const float t = sum_over_q(w[bl]);
+            mine = q == bl ? t : mine;
+        }
+        const int pos = tile * 64 + 16 * q + c;
+        if (pos < len) weights[pos] += mine;
+    }
+}
+
+// Rows of a block: 16 * MT. Sixty-four rows of 256 dims would need more registers than a wave has.
+static int row_tiles(int rows, int dim) { return rows <= 16 ? 1 : (rows <= 32 || dim == 256 ? 2 : 4); }
+
+// Splits of a (sequence, kv head, row block): enough workgroups for four on each of
+// the 256 CUs, but no split of fewer than two tiles for each of its four waves.
+static int split_count(long long blocks, int max_len) {
+    const long long tiles = ((long long)max_len + 63) / 64;
+    long long s = (1024 + blocks - 1) / blocks, most = tiles / (2 * kWaves);
+    s = s < most ? s : most;
+    return s < 1 ? 1 : (int)(s > 256 ? 256 : s);
+}
+
+struct Launch {
+    int mt, row_blocks, splits;
+    size_t part, ml, lse, total;
+};
+static Launch plan_of(const xp_kv_dims* d, int heads, int q_rows, int batch, int max_len) {
+    Launch p{};
+    const long long rows = (long long)q_rows * (heads / d->kv_heads);
+    p.mt = row_tiles(rows > 64 ? 64 : (int)rows, d->head_dim);
+    p.row_blocks = (int)((rows + 16 * p.mt - 1) / (16 * p.mt));
+    const long long blocks = (long long)batch * d->kv_heads * p.row_blocks;
+    p.splits = split_count(blocks < 1 ? 1 : blocks, max_len);
+    const size_t parts = p.splits > 1 ? (size_t)blocks * p.splits : 0;
+    p.part = 0;
+    p.ml = parts * 16 * p.mt * d->head_dim * sizeof(float);
+    p.lse = p.ml + align256(parts * 32 * p.mt * sizeof(float));
+    p.total = p.lse + align256((size_t)batch * heads * q_rows * sizeof(float));
+    return p;
+}
+
+static int check_decode(const xp_kv_dims* d, int heads, int q_rows, int batch, int max_pages, int max_len) {
+    const int st = kv::check_geo(d, batch, max_pages);
+    if (st != XP_OK) return st;
+    if (heads < 1 || heads > 65535 || heads % d->kv_heads || q_rows < 1 || q_rows > 65535 || max_len < 0) return XP_ERR_SHAPE;
+    const Launch p = plan_of(d, heads, q_rows, batch, max_len);
+    if ((long long)p.row_blocks * d->kv_heads > 65535) return XP_ERR_SHAPE;
+    return XP_OK;
+}
+
+template <int D, bool BF16>
+static int launch(const Args& a, const Launch& p, int batch, int max_len, hipStream_t s) {
+    const dim3 grid(p.splits, p.row_blocks * a.g.kv_heads, batch), block(256);
+    const dim3 join((16 * p.mt * D / 4 + 255) / 256, grid.y, batch);
+#define XP_ATTN_LAUNCH(MT_)                                                                        \
+    do {                                                                                           \
+        hipLaunchKernelGGL((attn_decode_kernel<D, MT_, BF16>), grid, block, 0, s, a);              \
+        if (p.splits > 1) hipLaunchKernelGGL((attn_join_kernel<D, MT_, BF16>), join, block, 0, s, a); \
+    } while (0)
+    if (p.mt == 1)
+        XP_ATTN_LAUNCH(1);
+    else if (p.mt == 2)
+        XP_ATTN_LAUNCH(2);
+    else if constexpr (D != 256)
+        XP_ATTN_LAUNCH(4);
+#undef XP_ATTN_LAUNCH
+    int rc = launch_status();
+    if (rc != XP_OK || !a.weights) return rc;
+    const long long tiles = ((long long)max_len + 63) / 64;
+    long long blocks = (tiles + 2 * kWaves - 1) / (2 * kWaves);
+    blocks = blocks < 1 ? 1 : (blocks > 1024 ? 1024 : blocks);
+    hipLaunchKernelGGL((attn_weights_kernel<D, BF16>), dim3((unsigned)blocks, a.g.kv_heads, batch), block, 0, s, a);
+    return launch_status();
+}
+
+}  // namespace attn
+}  // namespace xp
+
+using namespace xp;
+using namespace xp::attn;
+
+XP_API size_t xp_attn_decode_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_t batch,
+                                             int32_t max_len) {
+    if (check_decode(dims, heads, q_rows, batch, 1, max_len) != XP_OK) return 0;
+    return plan_of(dims, heads, q_rows, batch, max_len).total;
+}
+
+XP_API int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_t batch, int32_t max_pages,
+                          int32_t max_len, int32_t type, const void* q, int64_t q_stride, float scale, int32_t window,
+                          const uint8_t* cache, const int32_t* table, const int32_t* lens, void* out, int64_t out_stride,
+                          float* weights, int64_t w_stride, void* workspace, size_t ws_bytes, void* stream) {
+    const int st = check_decode(dims, heads, q_rows, batch, max_pages, max_len);
+    if (st != XP_OK) return st;
+    if ((type != XP_BF16 && type != XP_F16) || window < 0 || !(scale > 0.0f && scale < __builtin_inff())) return XP_ERR_SHAPE;
+    if (batch == 0) return XP_OK;
+    if (!q || !cache || !table || !lens || !out || !workspace) return XP_ERR_NULL;
+    const int64_t width = (int64_t)heads * dims->head_dim;
+    if (q_stride < width || out_stride < width || q_stride % 8 || out_stride % 4 || !kv::aligned_to(q, 16) ||
+        !kv::aligned_to(out, 8) || !kv::aligned_to(cache, 16) || !kv::aligned_to(table, 4) || !kv::aligned_to(lens, 4) ||
+        !kv::aligned_to(workspace, 16))
+        return XP_ERR_SHAPE;
+    if (weights && (w_stride < (int64_t)max_pages * dims->page || !kv::aligned_to(weights, 4))) return XP_ERR_SHAPE;
+    const Launch p = plan_of(dims, heads, q_rows, batch, max_len);
+    if (ws_bytes < p.total) return XP_ERR_WORKSPACE;
+    char* ws = (char*)workspace;
+    Args a{};
+    a.g = kv::geo_of(dims, max_pages);
+    a.q = q;
+    a.q_stride = q_stride;
+    a.cache = cache;
+    a.table = table;
+    a.lens = lens;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.part = (float*)(ws + p.part);
+    a.part_ml = (float*)(ws + p.ml);
+    a.lse = weights ? (float*)(ws + p.lse) : nullptr;
+    a.weights = weights;
+    a.w_stride = w_stride;
+    a.heads = heads;
+    a.group = heads / dims->kv_heads;
+    a.q_rows = q_rows;
+    a.row_blocks = p.row_blocks;
+    a.splits = p.splits;
+    a.window = window;
+    a.scale_m = (float)__builtin_frexp((double)scale * 1.4426950408889634, &a.scale_e);
+    hipStream_t s = (hipStream_t)stream;
+    const bool bf = type == XP_BF16;
+    switch (dims->head_dim) {
+        case 64: return bf ? launch<64, true>(a, p, batch, max_len, s) : launch<64, false>(a, p, batch, max_len, s);
+        case 128: return bf ? launch<128, true>(a, p, batch, max_len, s) : launch<128, false>(a, p, batch, max_len, s);
+        default: return bf ? launch<256, true>(a, p, batch, max_len, s) : launch<256, false>(a, p, batch, max_len, s);
+    }
+}

@@ -1,0 +1,356 @@
+// xp_attn_prompt.hip — causal attention over whole prompts, packed sequences of
+// different lengths, grouped heads, bf16 or fp16.
+//
+// One pass over the keys with a running maximum and sum. A row is a (token, head of
+// the kv head's group) pair, tokens first, so the heads that share keys share a
+// workgroup and a short prompt still fills its 128 rows. A wave owns 32 rows and
+// takes 64 positions at a time: S^T = K Q^T (v_mfma_f32_32x32x16, positions as the
+// matrix rows) leaves lane (m, hi) = (lane % 32, lane / 32) with row m at positions
+// 8 a + 4 hi + i of each 32, so the exponentials, once rounded, are the operand of
+// O^T += V^T P^T where they are: V follows the same order of positions through the
+// 16-bit transposing LDS read, which hands a lane four positions of one column.
+//
+// Scores, maxima, sums and outputs are fp32; exponentials round once to the type of
+// v (the product's operand), the result once to the output type.
+#include "xp_kv_dev.h"
+
+namespace xp {
+namespace prompt {
+
+typedef __attribute__((ext_vector_type(8))) _Float16 h16x8;
+typedef __attribute__((ext_vector_type(8))) __bf16 b16x8;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+
+constexpr int kRows = 128;   // rows of a workgroup: four waves of 32
+constexpr int kPos = 64;     // positions of a tile
+
+struct Args {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* out;
+    long long q_stride, k_stride, v_stride, out_stride;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int rows_q, rows_k, batch, kv_heads, group, window;
+    float scale_log2;
+};
+
+template <bool BF16>
+__device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h16x8, a), __builtin_bit_cast(h16x8, b), c, 0, 0, 0);
+}
+
+// 16 bits of the operand type, nearest even.
+template <bool BF16>
+__device__ __forceinline__ short half_of(float x) {
+    if constexpr (BF16) return __builtin_bit_cast(short, (__bf16)x);
+    return __builtin_bit_cast(short, (_Float16)x);
+}
+
+template <bool BF16>
+__device__ __forceinline__ bool not_finite(uint16_t u) {
+    constexpr uint16_t e = BF16 ? 0x7f80 : 0x7c00;
+    return (u & e) == e;
+}
+
+__device__ __forceinline__ float swap_max(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float swap_sum(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// LDS places. K: a row's 16-byte chunks are permuted so that 16 neighbouring rows at
+// one chunk index cover all banks; V: its 64-byte blocks, so that the eight rows of a
+// transposing read meet each bank twice at most.
+template <int D>
+__device__ __forceinline__ int k_at(int pos, int chunk) {
+    const int s = D == 64 ? (pos >> 1) & 7 : pos & 15;
+    return pos * (2 * D) + (chunk ^ s) * 16;
+}
+template <int D>
+__device__ __forceinline__ int v_at(int pos, int block) {
+    const int s = D == 64 ? (pos >> 1) & 1 : pos & 3;
+    return pos * (2 * D) + (block ^ s) * 64;
+}
+
+// The workgroup's block of rows: sequence and first row, the longest-running (last)
+// blocks of the packed batch first. false: no such block.
+__device__ __forceinline__ bool find_block(const Args& a, int blk, int& seq, int& first) {
+    const int lane = threadIdx.x & 63;
+    int total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        int before = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 64) {
+            const int b = b0 + lane;
+            int n = 0;
+            if (b < a.batch) {
+                const long long rows = (long long)a.cu_q[b + 1] - a.cu_q[b];
+                if (rows > 0 && rows <= a.rows_q) n = (int)((rows * a.group + kRows - 1) / kRows);
+            }
+            const int incl = wave_incl_sum(n);
+            if (pass == 1) {
+                const uint64_t hit = __ballot(n > 0 && before + incl - n <= blk && blk < before + incl);
+                if (hit) {
+                    const int l = __ffsll((unsigned long long)hit) - 1;
+                    seq = b0 + l;
+                    first = (blk - before - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l))) * kRows;
+                    return true;
+                }
+            }
+            before += __builtin_amdgcn_readlane(incl, 63);
+        }
+        if (pass == 0) {
+            total = before;
+            if (blk >= total) return false;
+            blk = total - 1 - blk;
+        }
+    }
+    return false;
+}
+
+template <int D, bool BF16>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args a) {
+    constexpr int NS = D / 16;                 // contraction steps of the scores
+    constexpr int ND = D / 32;                 // column blocks of the output
+    constexpr int NL = kPos * D / 8 / 256;     // 16-byte chunks a thread stages of each of k and v
+    __shared__ __attribute__((aligned(16))) uint8_t lk[kPos * D * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t lv[kPos * D * 2];
+
+    const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, hi = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int head = blockIdx.x % a.kv_heads;
+    int b, first;
+    if (!find_block(a, blockIdx.x / a.kv_heads, b, first)) return;
+    const int q0 = a.cu_q[b], nq = a.cu_q[b + 1] - q0;
+    if (q0 < 0 || (long long)q0 + nq > a.rows_q) return;
+    int k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+    k0 = k0 < 0 ? 0 : (k0 > a.rows_k ? a.rows_k : k0);
+    k1 = k1 < k0 ? k0 : (k1 > a.rows_k ? a.rows_k : k1);
+    const int nk = k1 - k0, shift = nk - nq;   // token i sits at position i + shift
+
+    const int rows = nq * a.group;
+    const int row = first + wave * 32 + m;
+    const bool live = row < rows;
+    const int tok = live ? row / a.group : 0;
+    const int hd = head * a.group + (live ? row - tok * a.group : 0);
+    const int at = live ? tok + shift : -1;    // the row's own position
+    const int lo = a.window > 0 && at - a.window + 1 > 0 ? at - a.window + 1 : 0;
+
+    s16x8 qf[NS];
+    const uint16_t* qp = a.q + (long long)(q0 + tok) * a.q_stride + (long long)hd * D + 8 * hi;
+#pragma unroll
+    for (int st = 0; st < NS; ++st) qf[st] = live ? *(const s16x8*)(qp + 16 * st) : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+
+    // tiles that some row of the workgroup sees, and those that all see whole
+    const int last_row = first + kRows < rows ? first + kRows - 1 : rows - 1;
+    const int at_first = first / a.group + shift, at_last = last_row / a.group + shift;
+    const int t_hi = at_last >= 0 ? (at_last >> 6) + 1 : 0;
+    const int w_first = at_first - a.window + 1, w_last = at_last - a.window + 1;
+    const int t_lo = a.window > 0 && w_first > 0 ? w_first >> 6 : 0;
+    const int full_lo = a.window > 0 && w_last > 0 ? w_last : 0, full_hi = at_first + 1;
+
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+    float mx = -__builtin_inff(), sum = 0.0f;
+
+    const uint16_t* kp = a.k + (long long)k0 * a.k_stride + (long long)head * D;
+    const uint16_t* vp = a.v + (long long)k0 * a.v_stride + (long long)head * D;
+    uint4 ck[NL], cv[NL];
+    auto fetch = [&](int tile) {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int c = j * 256 + tid, pos = c / (D / 8), ch = c % (D / 8), p = tile * kPos + pos;
+            ck[j] = p < nk ? *(const uint4*)(kp + (long long)p * a.k_stride + 8 * ch) : uint4{0, 0, 0, 0};
+            cv[j] = p < nk ? *(const uint4*)(vp + (long long)p * a.v_stride + 8 * ch) : uint4{0, 0, 0, 0};
+        }
+    };
+    if (t_lo < t_hi) fetch(t_lo);
+
+    for (int tile = t_lo; tile < t_hi; ++tile) {
+        const bool masked = tile * kPos < full_lo || tile * kPos + kPos > full_hi;
+        __syncthreads();                       // the last tile is read
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int c = j * 256 + tid, pos = c / (D / 8), ch = c % (D / 8);
+            *(uint4*)(lk + k_at<D>(pos, ch)) = ck[j];
+            *(uint4*)(lv + v_at<D>(pos, ch >> 2) + (ch & 3) * 16) = cv[j];
+            if (masked) {
+                const uint32_t u[4] = {cv[j].x, cv[j].y, cv[j].z, cv[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bad |= not_finite<BF16>((uint16_t)u[i]) || not_finite<BF16>((uint16_t)(u[i] >> 16));
+            }
+        }
+        // a value of v that is not finite must not meet the zero weight of a row that does not see it
+        if (masked)
+            bad = __syncthreads_or(bad);
+        else
+            __syncthreads();
+        if (tile + 1 < t_hi) fetch(tile + 1);
+
+        f32x16 s[2];
+#pragma unroll
+        for (int pb = 0; pb < 2; ++pb) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[pb][r] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < NS; ++st)
+                s[pb] = mma<BF16>(*(const s16x8*)(lk + k_at<D>(pb * 32 + m, 2 * st + hi)), qf[st], s[pb]);
+        }
+        if (masked) {
+#pragma unroll
+            for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int p = tile * kPos + pb * 32 + 8 * (r >> 2) + 4 * hi + (r & 3);
+                    if (p > at || p < lo) s[pb][r] = -__builtin_inff();
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int r = 1; r < 32; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
+        top = swap_max(top) * a.scale_log2;
+        if (__ballot(top > mx)) {
+            const float nm = fmaxf(top, mx);
+            const float alpha = __builtin_amdgcn_exp2f(mx - (nm == -__builtin_inff() ? 0.0f : nm));
+            mx = nm;
+            sum *= alpha;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] *= alpha;
+        }
+        const float base = mx == -__builtin_inff() ? 0.0f : -mx;
+        s16x8 p[4];
+        float add = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r >> 4][r & 15], a.scale_log2, base));
+            add += x;
+            p[r >> 3][r & 7] = half_of<BF16>(x);
+        }
+        sum += add;
+
+        const int i4 = (lane & 15) >> 2, col = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            f32x16 odd[3];                     // seen values of v that are +inf, -inf, NaN: their counts
+            const bool slow = masked && bad;
+            if (slow) {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) odd[e][r] = 0.0f;
+            }
+#pragma unroll
+            for (int st = 0; st < 4; ++st) {
+                const int pos = 16 * st + 4 * hi + i4;
+                const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4*)(lv + v_at<D>(pos, d) + col));
+                const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4*)(lv + v_at<D>(pos + 8, d) + col));
+                s16x8 vf = s16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+                if (slow) {
+                    constexpr short one = BF16 ? 0x3f80 : 0x3c00;
+                    constexpr uint16_t inf = BF16 ? 0x7f80 : 0x7c00;
+                    s16x8 f[3], seen;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint16_t u = (uint16_t)vf[j];
+                        f[0][j] = u == inf ? one : (short)0;
+                        f[1][j] = u == (inf | 0x8000) ? one : (short)0;
+                        f[2][j] = not_finite<BF16>(u) && (u & 0x7fff) != inf ? one : (short)0;
+                        if (not_finite<BF16>(u)) vf[j] = 0;
+                        const int ps = tile * kPos + 16 * st + 8 * (j >> 2) + 4 * hi + (j & 3);
+                        seen[j] = ps <= at && ps >= lo ? one : (short)0;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) odd[e] = mma<BF16>(f[e], seen, odd[e]);
+                }
+                o[d] = mma<BF16>(vf, p[st], o[d]);
+            }
+            if (slow) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float inf = __builtin_inff();
+                    if (odd[0][r] > 0.0f) o[d][r] += inf;
+                    if (odd[1][r] > 0.0f) o[d][r] -= inf;
+                    if (odd[2][r] > 0.0f) o[d][r] = __builtin_nanf("");
+                }
+            }
+        }
+    }
+
+    sum = swap_sum(sum);
+    if (!live) return;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;      // nothing seen: zeros
+    uint16_t* y = a.out + (long long)(q0 + tok) * a.out_stride + (long long)hd * D + 4 * hi;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                w[j] = (uint32_t)(uint16_t)half_of<BF16>(o[d][4 * e + 2 * j] * inv) |
+                       (uint32_t)(uint16_t)half_of<BF16>(o[d][4 * e + 2 * j + 1] * inv) << 16;
+            *(uint2*)(y + 32 * d + 8 * e) = uint2{w[0], w[1]};
+        }
+}
+
+}  // namespace prompt
+}  // namespace xp
+
+using namespace xp;
+using namespace xp::prompt;
+
+XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch, int32_t rows_q, int32_t rows_k,
+                          int32_t type, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, float scale, int32_t window,
+                          void* out, int64_t out_stride, void* stream) {
+    if (kv_heads < 1 || kv_heads > 1024 || heads < 1 || heads > 65535 || heads % kv_heads ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256) || batch < 0 || batch > 65535 || rows_q < 0 || rows_k < 0 ||
+        (type != XP_BF16 && type != XP_F16) || window < 0 || !(scale > 0.0f && scale < __builtin_inff()))
+        return XP_ERR_SHAPE;
+    const int group = heads / kv_heads;
+    const int64_t blocks = ((int64_t)rows_q * group + kRows - 1) / kRows + batch;
+    if ((int64_t)rows_q * group > 0x7fffffff - kRows || rows_k > 0x7fffffff - kPos || blocks * kv_heads > 0x7fffffff)
+        return XP_ERR_SHAPE;
+    if (batch == 0 || rows_q == 0) return XP_OK;
+    if (!q || !cu_q || !cu_k || !out || (rows_k > 0 && (!k || !v))) return XP_ERR_NULL;
+    const int64_t qw = (int64_t)heads * head_dim, kw = (int64_t)kv_heads * head_dim;
+    if (q_stride < qw || out_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
+        out_stride % 4 || !kv::aligned_to(q, 16) || !kv::aligned_to(k, 16) || !kv::aligned_to(v, 16) || !kv::aligned_to(out, 8) || !kv::aligned_to(cu_q, 4) || !kv::aligned_to(cu_k, 4))
+        return XP_ERR_SHAPE;
+    const Args a{(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)out, q_stride, k_stride, v_stride,
+                 out_stride, cu_q, cu_k, rows_q, rows_k, batch, kv_heads, group, window, kv::log2_scale(scale)};
+    const dim3 grid((unsigned)(blocks * kv_heads)), block(256);
+    hipStream_t s = (hipStream_t)stream;
+#define XP_PROMPT_LAUNCH(D_)                                                                       \
+    do {                                                                                           \
+        if (type == XP_BF16)                                                                       \
+            hipLaunchKernelGGL((attn_prompt_kernel<D_, true>), grid, block, 0, s, a);              \
+        else                                                                                       \
+            hipLaunchKernelGGL((attn_prompt_kernel<D_, false>), grid, block, 0, s, a);             \
+    } while (0)
+    if (head_dim == 64)
+        XP_PROMPT_LAUNCH(64);
+    else if (head_dim == 128)
+        XP_PROMPT_LAUNCH(128);
+    else
+        XP_PROMPT_LAUNCH(256);
+#undef XP_PROMPT_LAUNCH
+    return launch_status();
+}

@@ -1,0 +1,106 @@
+// xp_kv_dev.h — the 4-bit key/value cache: geometry, layout and codec shared by
+// the cache operators (xp_kv.hip) and decode attention (xp_attn.hip).
+//
+// A cache is n_pages pages of `page` positions; a page holds, for every kv head
+// in turn, page / 64 tiles of 64 positions. With NG = head_dim / 32 groups of 32
+// values a tile is NG * 2176 bytes (4.25 bits a value):
+//   K codes   16-byte chunk (pos, g) at g*1024 + pos*16, byte b = values 2b (low
+//             nibble) and 2b + 1 of group g: the packed weights' chunk. A lane of
+//             the score product takes one chunk, so its values share one scale.
+//   K scales  byte (pos, g) at NG*1024 + g*64 + (pos%16)*4 + pos/16: the four
+//             16-position blocks a lane works on are one dword.
+//   V codes   8-byte chunk (pos, h) at NG*1088 + h*512 + pos*8, h = 16 values:
+//             the row of a 4-bit transposing LDS read; consecutive positions are
+//             consecutive 8-byte words, so those reads meet no bank twice.
+//   V scales  byte (pos, g) at NG*2112 + g*64 + (pos/4%4)*16 + (pos/16)*4 + pos%4:
+//             the 16 positions a lane holds probabilities of are 16 bytes in order.
+#pragma once
+
+#include "xp_common.h"
+
+namespace xp {
+namespace kv {
+
+constexpr int kTilePos = 64;
+
+struct Geo {
+    int kv_heads;
+    int groups;      // head_dim / 32
+    int page;        // positions per page
+    int n_pages;
+    int max_pages;   // columns of the page table
+};
+
+__host__ __device__ __forceinline__ int tile_bytes(int groups) { return groups * 2176; }
+
+// Where position pos (0 <= pos < max_pages * page) of a sequence lies: the byte
+// offset of its tile, or -1 when its page is not one of the cache's.
+__device__ __forceinline__ long long tile_at(const Geo& g, const int32_t* table_row, int head, int pos) {
+    const int col = pos / g.page;
+    const int id = table_row[col];
+    if ((unsigned)id >= (unsigned)g.n_pages) return -1;
+    const int tiles = g.page / kTilePos;
+    return (((long long)id * g.kv_heads + head) * tiles + (pos - col * g.page) / kTilePos) * tile_bytes(g.groups);
+}
+
+__device__ __forceinline__ int k_code(int groups, int pos, int g) { return g * 1024 + pos * 16; }
+__device__ __forceinline__ int k_scale(int groups, int pos, int g) {
+    return groups * 1024 + g * 64 + (pos & 15) * 4 + (pos >> 4);
+}
+__device__ __forceinline__ int v_code(int groups, int pos, int h) { return groups * 1088 + h * 512 + pos * 8; }
+__device__ __forceinline__ int v_scale(int groups, int pos, int g) {
+    return groups * 2112 + g * 64 + ((pos >> 2) & 3) * 16 + (pos >> 4) * 4 + (pos & 3);
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0); }
+
+// The smallest E4M3FN scale s with 6 s >= amax (amax >= 0), 448 when there is
+// none, the NaN byte when amax is not finite. amax / 6 in fp32 places s within a
+// step; six times an E4M3 value is exact, so the comparisons decide it exactly.
+__device__ __forceinline__ uint32_t scale_byte(float amax) {
+    const float r = amax * (1.0f / 6.0f);
+    int code = r >= 0x1p-6f ? (int)(__float_as_uint(r) >> 20) - ((127 - 7) << 3) : (int)(r * 512.0f);
+    code = code > 0x7e ? 0x7e : code;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (code < 0x7e && 6.0f * e4m3_value((uint32_t)code) < amax) ++code;
+    return (__float_as_uint(amax) & 0x7f800000u) == 0x7f800000u ? 0x7fu : (uint32_t)code;
+}
+
+// The e2m1 code nearest to v / s, ties to the even code, beyond 6 s to 6 s. The
+// seven midpoints times an E4M3 scale are exact in fp32, so no quotient is rounded.
+__device__ __forceinline__ uint32_t e2m1_code(float v, float s) {
+    const float a = __builtin_fabsf(v);
+    uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) +
+                 (a >= 3.5f * s) + (a > 5.0f * s);
+    c = s > 0.0f ? c : 0u;   // zero group, or a NaN scale
+    return c | (__float_as_uint(v) >> 31 << 3);
+}
+
+inline bool geo_ok(const xp_kv_dims* d) {
+    return d->kv_heads >= 1 && d->kv_heads <= 1024 && (d->head_dim == 64 || d->head_dim == 128 || d->head_dim == 256) &&
+           d->page >= kTilePos && d->page % kTilePos == 0 && d->page <= (1 << 20) && d->n_pages >= 1;
+}
+
+// Shared checks of the calls that take a page table.
+inline int check_geo(const xp_kv_dims* d, int32_t batch, int32_t max_pages) {
+    if (!d) return XP_ERR_NULL;
+    if (!geo_ok(d) || batch < 0 || batch > 65535 || max_pages < 1) return XP_ERR_SHAPE;
+    if ((long long)max_pages * d->page > 0x7fffffffLL - 1024) return XP_ERR_SHAPE;
+    return XP_OK;
+}
+
+inline Geo geo_of(const xp_kv_dims* d, int32_t max_pages) {
+    return Geo{d->kv_heads, d->head_dim / 32, d->page, d->n_pages, max_pages};
+}
+
+// scale * log2(e), kept a normal number: neither 0 nor infinity may meet a masked -inf or a score of 0.
+inline float log2_scale(float scale) {
+    const double x = (double)scale * 1.4426950408889634;
+    return (float)(x < 0x1p-126 ? 0x1p-126 : (x > 0x1p127 ? 0x1p127 : x));
+}
+
+inline bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+}  // namespace kv
+}  // namespace xp

@@ -25,12 +25,23 @@ EXPORTS = (
     "xp_prefill_gateup", "xp_prefill_down", "xp_fp8_packed_bytes", "xp_fp8_pack", "xp_fp8_rows",
     "xp_gateup_rows_act16", "xp_down_rows_act16", "xp_combine_y16", "xp_fp8_rows_f32", "xp_stream_weights",
     "xp_decode_static", "xp_gateup_rows_coded", "xp_fp8_rows_multi",
+    "xp_kv_bytes", "xp_kv_append", "xp_kv_read", "xp_kv_evict", "xp_attn_decode_workspace_bytes", "xp_attn_decode",
+    "xp_attn_prompt",
 )
 
 
 class xp_fp8_matrix(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("y", ctypes.c_void_p)]
+
+
+class xp_kv_dims(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32)]
+
+    def __repr__(self):
+        return "xp_kv_dims(kv_heads=%d, head_dim=%d, page=%d, n_pages=%d)" % (
+            self.kv_heads, self.head_dim, self.page, self.n_pages)
 
 
 class XPError(RuntimeError):
@@ -90,6 +101,18 @@ def lib():
         L.xp_decode_static.argtypes = [D, i32, P, P, P, P, P, P, P, P, P]
         L.xp_gateup_rows_coded.argtypes = [D, i32, P, P, P, P, sz, P, P]
         L.xp_fp8_rows_multi.argtypes = [i32, i32, P, ctypes.POINTER(xp_fp8_matrix), i32, i32, P]
+        i64, KD = ctypes.c_int64, ctypes.POINTER(xp_kv_dims)
+        L.xp_kv_bytes.argtypes = [KD]
+        L.xp_kv_bytes.restype = sz
+        L.xp_kv_append.argtypes = [KD, i32, i32, i32, i32, P, i64, P, i64, P, P, P, P, P]
+        L.xp_kv_read.argtypes = [KD, i32, i32, i32, i32, P, P, P, P, P, i64, P, i64, P]
+        L.xp_kv_evict.argtypes = [KD, i32, i32, P, P, P, P, i64, i32, i32, i32, i32, P, P, P, P, i64, P]
+        L.xp_attn_decode_workspace_bytes.argtypes = [KD, i32, i32, i32, i32]
+        L.xp_attn_decode_workspace_bytes.restype = sz
+        L.xp_attn_decode.argtypes = [KD, i32, i32, i32, i32, i32, i32, P, i64, ctypes.c_float, i32, P, P, P, P, i64, P,
+                                     i64, P, sz, P]
+        L.xp_attn_prompt.argtypes = [i32, i32, i32, i32, i32, i32, i32, P, i64, P, i64, P, i64, P, P, ctypes.c_float,
+                                     i32, P, i64, P]
         L.xp_set_tiers.argtypes = [P, i32, P, i32]
         L.xp_get_tiers.argtypes = [P, P, P, P]
         L.xp_status_string.argtypes = [ctypes.c_int]
@@ -99,7 +122,8 @@ def lib():
                      "xp_route_gateup", "xp_down_combine", "xp_prefill_gateup", "xp_prefill_down",
                      "xp_fp8_pack", "xp_fp8_rows", "xp_gateup_rows_act16", "xp_down_rows_act16",
                      "xp_combine_y16", "xp_fp8_rows_f32", "xp_stream_weights", "xp_decode_static",
-                     "xp_gateup_rows_coded", "xp_fp8_rows_multi"):
+                     "xp_gateup_rows_coded", "xp_fp8_rows_multi", "xp_kv_append", "xp_kv_read", "xp_kv_evict",
+                     "xp_attn_decode", "xp_attn_prompt"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
         try:
@@ -444,6 +468,162 @@ def xp_fp8_rows_multi(rows: int, k: int, x, mats, slices: int = 0, stream=None) 
         _dev_bf16(x, "x", rows * k)
     _check(lib().xp_fp8_rows_multi(int(rows), int(k), _ptr(x), arr, len(mats), int(slices), _stream(stream)),
            "xp_fp8_rows_multi")
+
+
+# ------------------------------------------- 4-bit key/value cache and attention
+XP_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def kv_dims(kv_heads: int, head_dim: int, page: int, n_pages: int) -> xp_kv_dims:
+    return xp_kv_dims(kv_heads, head_dim, page, n_pages)
+
+
+def xp_kv_bytes(d: xp_kv_dims) -> int:
+    return int(lib().xp_kv_bytes(ctypes.byref(d)))
+
+
+def _rows3(t, dtype, name: str, rows: int, heads: int, dim: int) -> int:
+    """A device tensor [rows][heads][dim] whose rows may lie apart; the stride between them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != (rows, heads, dim):
+        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, dim, list(t.shape)))
+    st = t.stride()
+    if (st[2] != 1 or (heads > 1 and st[1] != dim)) and t.numel():
+        raise ValueError("%s: a row's heads must be contiguous" % name)
+    return st[0] if rows > 1 else heads * dim
+
+
+def _table(t, name: str = "table"):
+    """A page table [batch][columns]."""
+    _dev(t, torch.int32, name)
+    if t.dim() != 2:
+        raise ValueError("%s must be [batch][pages of a sequence]" % name)
+    return t.shape
+
+
+def _type(t, name: str, types) -> int:
+    dt = getattr(t, "dtype", None)
+    if dt not in types:
+        raise ValueError("%s must be one of %s" % (name, ", ".join(str(x) for x in types)))
+    return XP_TYPES[dt]
+
+
+def _on(first, *others):
+    """The device guard of a call: all its tensors lie on one device, which need not be the current one."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors on %s and %s in one call" % (first.device, t.device))
+    return torch.cuda.device(first.device)
+
+
+def _cache(d: xp_kv_dims, cache) -> None:
+    _dev(cache, torch.uint8, "cache", xp_kv_bytes(d))
+
+
+def xp_kv_append(d: xp_kv_dims, k, v, cu_rows, start, table, cache, stream=None) -> None:
+    """Quantise the packed rows k, v [rows][kv_heads][head_dim] into the cache (see xp.h)."""
+    ty = _type(k, "k", tuple(XP_TYPES))
+    batch, cols = _table(table)
+    rows = k.shape[0]
+    ks = _rows3(k, k.dtype, "k", rows, d.kv_heads, d.head_dim)
+    vs = _rows3(v, k.dtype, "v", rows, d.kv_heads, d.head_dim)
+    _dev(cu_rows, torch.int32, "cu_rows", batch + 1)
+    _dev(start, torch.int32, "start", batch)
+    _cache(d, cache)
+    with _on(cache, k, v, cu_rows, start, table):
+        _check(lib().xp_kv_append(ctypes.byref(d), batch, cols, rows, ty, _ptr(k), ks, _ptr(v), vs, _ptr(cu_rows),
+                                  _ptr(start), _ptr(table), _ptr(cache), _stream(stream)), "xp_kv_append")
+
+
+def xp_kv_read(d: xp_kv_dims, cu_rows, start, table, cache, k, v, stream=None) -> None:
+    """Read cached rows back into k, v [rows][kv_heads][head_dim] (see xp.h)."""
+    ty = _type(k, "k", tuple(XP_TYPES))
+    batch, cols = _table(table)
+    rows = k.shape[0]
+    ks = _rows3(k, k.dtype, "k", rows, d.kv_heads, d.head_dim)
+    vs = _rows3(v, k.dtype, "v", rows, d.kv_heads, d.head_dim)
+    _dev(cu_rows, torch.int32, "cu_rows", batch + 1)
+    _dev(start, torch.int32, "start", batch)
+    _cache(d, cache)
+    with _on(cache, k, v, cu_rows, start, table):
+        _check(lib().xp_kv_read(ctypes.byref(d), batch, cols, rows, ty, _ptr(cu_rows), _ptr(start), _ptr(table),
+                                _ptr(cache), _ptr(k), ks, _ptr(v), vs, _stream(stream)), "xp_kv_read")
+
+
+def _weights(w, name: str, batch: int, kv_heads: int, least: int) -> int:
+    """Accumulated weights fp32 [batch][kv_heads][columns], contiguous; the stride of a row."""
+    _dev(w, torch.float32, name)
+    if w.dim() != 3 or w.shape[0] != batch or w.shape[1] != kv_heads or w.shape[2] < least:
+        raise ValueError("%s must be [%d, %d, at least %d], got %s" % (name, batch, kv_heads, least, list(w.shape)))
+    return w.shape[2]
+
+
+def xp_kv_evict(d: xp_kv_dims, cache, table, lens, weights, keep: int, dst_table, kept, lens_out, weights_out,
+                sinks: int = 0, recent: int = 0, stream=None) -> None:
+    """Cut sequences to ``keep`` positions by accumulated weight (see xp.h)."""
+    batch, cols = _table(table)
+    dbatch, dcols = _table(dst_table, "dst_table")
+    if dbatch != batch:
+        raise ValueError("dst_table has %d sequences, table %d" % (dbatch, batch))
+    ws = _weights(weights, "weights", batch, d.kv_heads, cols * d.page)
+    wo = _weights(weights_out, "weights_out", batch, d.kv_heads, int(keep))
+    _dev(lens, torch.int32, "lens", batch)
+    _dev(lens_out, torch.int32, "lens_out", batch)
+    _dev(kept, torch.int32, "kept", batch * d.kv_heads * int(keep))
+    _cache(d, cache)
+    with _on(cache, table, lens, weights, dst_table, kept, lens_out, weights_out):
+        _check(lib().xp_kv_evict(ctypes.byref(d), batch, cols, _ptr(cache), _ptr(table), _ptr(lens), _ptr(weights), ws,
+                                 int(keep), int(sinks), int(recent), dcols, _ptr(dst_table), _ptr(kept),
+                                 _ptr(lens_out), _ptr(weights_out), wo, _stream(stream)), "xp_kv_evict")
+
+
+def xp_attn_decode_workspace_bytes(d: xp_kv_dims, heads: int, q_rows: int, batch: int, max_len: int) -> int:
+    return int(lib().xp_attn_decode_workspace_bytes(ctypes.byref(d), int(heads), int(q_rows), int(batch),
+                                                    int(max_len)))
+
+
+def xp_attn_decode(d: xp_kv_dims, q, cache, table, lens, max_len: int, scale: float, out, workspace, q_rows: int = 1,
+                   window: int = 0, weights=None, stream=None) -> None:
+    """Attention of q [batch * q_rows][heads][head_dim] over the 4-bit cache (see xp.h)."""
+    ty = _type(q, "q", (torch.bfloat16, torch.float16))
+    batch, cols = _table(table)
+    heads = q.shape[1] if q.dim() == 3 else 0
+    qs = _rows3(q, q.dtype, "q", batch * int(q_rows), heads, d.head_dim)
+    os_ = _rows3(out, q.dtype, "out", batch * int(q_rows), heads, d.head_dim)
+    _dev(lens, torch.int32, "lens", batch)
+    _dev(workspace, torch.uint8, "workspace")
+    _cache(d, cache)
+    ws = 0 if weights is None else _weights(weights, "weights", batch, d.kv_heads, cols * d.page)
+    with _on(cache, q, table, lens, out, workspace, weights):
+        _check(lib().xp_attn_decode(ctypes.byref(d), heads, int(q_rows), batch, cols, int(max_len), ty, _ptr(q), qs,
+                                    scale, int(window), _ptr(cache), _ptr(table), _ptr(lens), _ptr(out), os_,
+                                    _ptr(weights), ws, _ptr(workspace), workspace.numel(), _stream(stream)),
+               "xp_attn_decode")
+
+
+def xp_attn_prompt(q, k, v, cu_q, cu_k, scale: float, out, window: int = 0, stream=None) -> None:
+    """Causal attention over packed prompts: q, out [rows_q][heads][head_dim], k, v
+    [rows_k][kv_heads][head_dim] (see xp.h)."""
+    ty = _type(q, "q", (torch.bfloat16, torch.float16))
+    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("q and k must be [rows][heads][head_dim]")
+    rows_q, heads, dim = q.shape
+    rows_k, kv_heads = k.shape[0], k.shape[1]
+    qs = _rows3(q, q.dtype, "q", rows_q, heads, dim)
+    ks = _rows3(k, q.dtype, "k", rows_k, kv_heads, dim)
+    vs = _rows3(v, q.dtype, "v", rows_k, kv_heads, dim)
+    os_ = _rows3(out, q.dtype, "out", rows_q, heads, dim)
+    _dev(cu_q, torch.int32, "cu_q")
+    _dev(cu_k, torch.int32, "cu_k", cu_q.numel())
+    if cu_q.numel() < 1:
+        raise ValueError("cu_q must hold the ends of each sequence, from 0")
+    with _on(q, k, v, cu_q, cu_k, out):
+        _check(lib().xp_attn_prompt(heads, kv_heads, dim, cu_q.numel() - 1, rows_q, rows_k, ty, _ptr(q), qs, _ptr(k),
+                                    ks, _ptr(v), vs, _ptr(cu_q), _ptr(cu_k), scale, int(window), _ptr(out), os_,
+                                    _stream(stream)), "xp_attn_prompt")
 
 
 # -------------------------------------------------------------- conveniences

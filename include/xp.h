@@ -329,6 +329,123 @@ typedef struct {
 int xp_fp8_rows_multi(int32_t rows, int32_t k, const uint16_t* x, const xp_fp8_matrix* mats, int32_t count,
                       int32_t slices, void* stream);
 
+/* --------------------------------------------- 4-bit key/value cache
+ * Keys and values of past positions in the weights' own format: e2m1 codes with
+ * one E4M3 scale per 32 values along the head dimension, 4.25 bits a value, in
+ * pages that a page table strings together for each sequence.
+ *
+ * Cache: n_pages pages, each [kv_heads][page / 64] tiles of 64 positions. With
+ * NG = head_dim / 32 a tile is NG * 2176 bytes:
+ *   K codes   16-byte chunk (pos, g) at g*1024 + pos*16, byte b holding values 2b
+ *             (low nibble) and 2b + 1 of group g;
+ *   K scales  byte (pos, g) at NG*1024 + g*64 + (pos%16)*4 + pos/16;
+ *   V codes   8-byte chunk (pos, h) at NG*1088 + h*512 + pos*8, 16 values each;
+ *   V scales  byte (pos, g) at NG*2112 + g*64 + (pos/4%4)*16 + (pos/16)*4 + pos%4.
+ * The cache buffer is 16-byte aligned, xp_kv_bytes long, and needs no initial value.
+ *
+ * Page table: int32 [batch][max_pages]; position p of sequence b lies on page
+ * table[b][p / page]. An entry outside [0, n_pages) is no page: positions there
+ * are not written, read as 0 and are not attended. Two entries in use must not
+ * name the same page, except where every call only reads it.
+ * head_dim is 64, 128 or 256; page a positive multiple of 64; batch at most 65,535.
+ *
+ * Element types of rows and the calls that take them are named with each call.
+ * A row stride is in elements from one row (token) to the next; heads of a row
+ * lie head_dim apart. Rows are read and written in 16-byte pieces: pointers must
+ * be 16-byte aligned and strides a multiple of 16 bytes (8 bytes for the out of
+ * the attention calls), else XP_ERR_SHAPE. */
+typedef enum { XP_BF16 = 0, XP_F16 = 1, XP_F32 = 2 } xp_type;
+
+typedef struct {
+    int32_t kv_heads; /* 1..1024 */
+    int32_t head_dim; /* 64, 128 or 256 */
+    int32_t page;     /* positions per page */
+    int32_t n_pages;  /* pages of the cache */
+} xp_kv_dims;
+
+/* Bytes of the cache buffer (host, pure; 0 on bad dims). */
+size_t xp_kv_bytes(const xp_kv_dims* dims);
+
+/* Quantise packed rows into the cache. k, v: [rows][kv_heads][head_dim] of `type`
+ * (any xp_type). cu_rows int32 [batch + 1], from 0, not falling: sequence b owns
+ * rows cu_rows[b] .. cu_rows[b+1] - 1, which go to its positions start[b],
+ * start[b] + 1, ... Rows from cu_rows[batch] on, and rows whose position is below
+ * 0 or at or beyond max_pages * page, go nowhere; nothing else of the cache changes.
+ * For each 32 values: the scale is the smallest E4M3FN value s with 6 s >= max |x|
+ * (448 if there is none: values beyond 6 * 448 are held as that), and each code the
+ * nearest e2m1 multiple of s, ties to the even code; a group with an infinity or
+ * NaN gets a NaN scale. All comparisons are exact. */
+int xp_kv_append(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, int32_t type, const void* k,
+                 int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_rows, const int32_t* start,
+                 const int32_t* table, uint8_t* cache, void* stream);
+
+/* The reverse, for the same row map: the cached values as `type` (any xp_type; all
+ * three hold them exactly). Rows whose position the cache does not have are 0; rows
+ * from cu_rows[batch] on are left as they were. A prompt's next piece reads its
+ * prefix back with it for xp_attn_prompt. */
+int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, int32_t type,
+               const int32_t* cu_rows, const int32_t* start, const int32_t* table, const uint8_t* cache, void* k,
+               int64_t k_stride, void* v, int64_t v_stride, void* stream);
+
+/* Cut sequences to at most `keep` positions by accumulated attention weight
+ * (xp_attn_decode's `weights`), for every kv head on its own. A sequence of at most
+ * keep positions keeps all; a longer one keeps its first `sinks`, its last `recent`
+ * and, between them, those of the largest weights (equal weights: lower positions
+ * first; NaN below every number), all in their order. sinks + recent <= keep.
+ *   kept        int32 [batch][kv_heads][keep]: the kept positions ascending, then -1;
+ *   cache       the kept positions' codes and scales move to positions 0, 1, ... of
+ *               dst_table [batch][dst_pages] in the same cache (room for keep positions);
+ *   lens_out    int32 [batch]: min(lens, keep); may be lens;
+ *   weights_out fp32 [batch][kv_heads] rows of wo_stride: the kept weights, then 0 up to
+ *               the old length (or the row's end); may be weights, with the same stride.
+ * The destination pages are either the source's own, entry for entry (as far as they
+ * go), or pages that no source entry names. weights: rows of w_stride >= max_pages *
+ * page fp32. lens are taken as between 0 and max_pages * page. */
+int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, uint8_t* cache, const int32_t* table,
+                const int32_t* lens, const float* weights, int64_t w_stride, int32_t keep, int32_t sinks,
+                int32_t recent, int32_t dst_pages, const int32_t* dst_table, int32_t* kept, int32_t* lens_out,
+                float* weights_out, int64_t wo_stride, void* stream);
+
+/* ------------------------------------------------------------ attention
+ * out = softmax(scale * q k^T over the visible positions) v, for heads query heads
+ * that share kv_heads key/value heads (head h reads kv head h / (heads / kv_heads)).
+ * A row at position p sees positions <= p of its sequence, with window > 0 only the
+ * last `window` of them. A row that sees nothing is 0, and so is one all of whose
+ * scores are -infinity. What a row does not see never reaches it, NaN and infinities
+ * included. scale is finite and > 0. Statistics and sums are fp32. */
+
+/* Bytes of workspace of an xp_attn_decode call with these arguments (host, pure; 0 on
+ * bad ones). It does not grow evenly with them: ask for each call's own values. */
+size_t xp_attn_decode_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_t batch,
+                                      int32_t max_len);
+
+/* Attention of q_rows query tokens per sequence over the 4-bit cache. q, out:
+ * [batch * q_rows][heads][head_dim] bf16 or fp16 (`type`), sequence b's tokens at rows
+ * b * q_rows on; the tokens' own k and v are in the cache already: token i sits at
+ * position lens[b] - q_rows + i. lens int32 [batch], taken as between 0 and
+ * max_pages * page; 0 for an idle slot. max_len (host) sizes the launch: no length
+ * should exceed it, and one that does is computed all the same, only slower.
+ * weights (or NULL): fp32 [batch][kv_heads] rows of w_stride >= max_pages * page; the
+ * call adds to each position the probabilities of all the kv head's rows there.
+ * workspace: 16-byte aligned, needs no initial value; calls that share it must not
+ * overlap. Results do not depend on the launch's timing. */
+int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_t batch, int32_t max_pages,
+                   int32_t max_len, int32_t type, const void* q, int64_t q_stride, float scale, int32_t window,
+                   const uint8_t* cache, const int32_t* table, const int32_t* lens, void* out, int64_t out_stride,
+                   float* weights, int64_t w_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/* Causal attention over packed prompts. q, out: [rows_q][heads][head_dim], k, v:
+ * [rows_k][kv_heads][head_dim], all bf16 or all fp16 (`type`); head_dim 64, 128 or
+ * 256. cu_q, cu_k int32 [batch + 1], from 0, not falling: sequence b owns the rows
+ * cu_q[b] .. cu_q[b+1] - 1 of q and out and cu_k[b] .. cu_k[b+1] - 1 of k and v.
+ * Its last query sits at its last key's position, so a prompt's later piece may
+ * attend to the earlier pieces' keys; a query before its first key sees nothing.
+ * Rows of out from cu_q[batch] on are left as they were. */
+int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch, int32_t rows_q, int32_t rows_k,
+                   int32_t type, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, float scale, int32_t window, void* out,
+                   int64_t out_stride, void* stream);
+
 /* ------------------------------------------------------ measurement probe */
 
 /* Bandwidth probe (not part of the layer): read every byte of the packed
