@@ -84,6 +84,52 @@ __device__ __forceinline__ int v_at(int pos, int block) {
     return pos * (2 * D) + (block ^ s) * 64;
 }
 
+__device__ __forceinline__ s16x8 v_frag(const uint8_t* a, const uint8_t* b) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)b);
+    return s16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+}
+
+// A tile that some row does not see whole and that holds values of v that are not
+// finite: a zero weight times one of those is NaN, so they are taken out of the tile
+// and added here, to the rows that see them. One product per kind (+inf, -inf, NaN)
+// of its places with what each row sees counts the seen ones of each column.
+template <int D, bool BF16>
+__device__ __forceinline__ void set_apart(f32x16 (&o)[D / 32], const uint8_t* lv, int first, int at, int lo) {
+    constexpr short one = BF16 ? 0x3f80 : 0x3c00;
+    constexpr uint16_t inf = BF16 ? 0x7f80 : 0x7c00;
+    const int lane = threadIdx.x & 63, hi = lane >> 5;
+    const int i4 = (lane & 15) >> 2, col = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll 1
+        for (int kind = 0; kind < 3; ++kind) {
+            f32x16 n;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) n[r] = 0.0f;
+#pragma unroll 1
+            for (int st = 0; st < 4; ++st) {
+                const int pos = 16 * st + 4 * hi + i4;
+                const s16x8 vf = v_frag(lv + v_at<D>(pos, d) + col, lv + v_at<D>(pos + 8, d) + col);
+                s16x8 f, seen;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint16_t u = (uint16_t)vf[j];
+                    const bool is = kind == 0 ? u == inf : (kind == 1 ? u == (inf | 0x8000)
+                                                                      : not_finite<BF16>(u) && (u & 0x7fff) != inf);
+                    f[j] = is ? one : (short)0;
+                    const int ps = first + 16 * st + 8 * (j >> 2) + 4 * hi + (j & 3);
+                    seen[j] = ps <= at && ps >= lo ? one : (short)0;
+                }
+                n = mma<BF16>(f, seen, n);
+            }
+            const float add = kind == 0 ? __builtin_inff() : (kind == 1 ? -__builtin_inff() : __builtin_nanf(""));
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (n[r] > 0.0f) o[d][r] += add;
+        }
+}
+
 // The workgroup's block of rows: sequence and first row, the longest-running (last)
 // blocks of the packed batch first. false: no such block.
 __device__ __forceinline__ bool find_block(const Args& a, int blk, int& seq, int& first) {
@@ -243,54 +289,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
         }
         sum += add;
 
+        if (masked && bad) {
+            set_apart<D, BF16>(o, lv, tile * kPos, at, lo);
+            __syncthreads();                   // every wave has seen the tile as it was
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const int c = j * 256 + tid, pos = c / (D / 8), ch = c % (D / 8);
+                uint16_t* e = (uint16_t*)(lv + v_at<D>(pos, ch >> 2) + (ch & 3) * 16);
+                for (int i = 0; i < 8; ++i)
+                    if (not_finite<BF16>(e[i])) e[i] = 0;
+            }
+            __syncthreads();
+        }
         const int i4 = (lane & 15) >> 2, col = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            f32x16 odd[3];                     // seen values of v that are +inf, -inf, NaN: their counts
-            const bool slow = masked && bad;
-            if (slow) {
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) odd[e][r] = 0.0f;
-            }
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int st = 0; st < 4; ++st) {
                 const int pos = 16 * st + 4 * hi + i4;
-                const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)(lv + v_at<D>(pos, d) + col));
-                const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)(lv + v_at<D>(pos + 8, d) + col));
-                s16x8 vf = s16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-                if (slow) {
-                    constexpr short one = BF16 ? 0x3f80 : 0x3c00;
-                    constexpr uint16_t inf = BF16 ? 0x7f80 : 0x7c00;
-                    s16x8 f[3], seen;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint16_t u = (uint16_t)vf[j];
-                        f[0][j] = u == inf ? one : (short)0;
-                        f[1][j] = u == (inf | 0x8000) ? one : (short)0;
-                        f[2][j] = not_finite<BF16>(u) && (u & 0x7fff) != inf ? one : (short)0;
-                        if (not_finite<BF16>(u)) vf[j] = 0;
-                        const int ps = tile * kPos + 16 * st + 8 * (j >> 2) + 4 * hi + (j & 3);
-                        seen[j] = ps <= at && ps >= lo ? one : (short)0;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) odd[e] = mma<BF16>(f[e], seen, odd[e]);
-                }
-                o[d] = mma<BF16>(vf, p[st], o[d]);
+                o[d] = mma<BF16>(v_frag(lv + v_at<D>(pos, d) + col, lv + v_at<D>(pos + 8, d) + col), p[st], o[d]);
             }
-            if (slow) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float inf = __builtin_inff();
-                    if (odd[0][r] > 0.0f) o[d][r] += inf;
-                    if (odd[1][r] > 0.0f) o[d][r] -= inf;
-                    if (odd[2][r] > 0.0f) o[d][r] = __builtin_nanf("");
-                }
-            }
-        }
     }
 
     sum = swap_sum(sum);
