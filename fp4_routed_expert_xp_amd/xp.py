@@ -482,26 +482,44 @@ def xp_kv_bytes(d: xp_kv_dims) -> int:
     return int(lib().xp_kv_bytes(ctypes.byref(d)))
 
 
-def _rows3(t, dtype, name: str, rows: int, heads: int, dim: int) -> int:
-    """A device tensor [rows][heads][dim] whose rows may lie apart; the stride between them."""
+# The checks below run once for every call of a decode step, whose kernels take a
+# few microseconds: plain attribute reads, and words only once something is wrong.
+def _refuse(t, dtype, name: str, numel: int, dev: int) -> None:
+    _dev(t, dtype, name, numel)
+    raise ValueError("%s is on device %d, the call's first tensor on device %d" % (name, t.get_device(), dev))
+
+
+def _arg(t, dtype, name: str, numel: int, dev: int) -> int:
+    """Address of a contiguous tensor of at least numel elements on device dev."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or dev < 0
+            or t.numel() < numel or not t.is_contiguous()):
+        _refuse(t, dtype, name, numel, dev)
+    return t.data_ptr()
+
+
+def _rows3(t, dtype, name: str, rows: int, heads: int, dim: int, dev: int):
+    """A device tensor [rows][heads][dim] whose rows may lie apart: (address, stride between rows)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != (rows, heads, dim):
         raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, dim, list(t.shape)))
+    if t.get_device() != dev:
+        _refuse(t, dtype, name, 0, dev)
     st = t.stride()
-    if (st[2] != 1 or (heads > 1 and st[1] != dim)) and t.numel():
+    if (st[2] != 1 or (st[1] != dim and heads > 1)) and t.numel():
         raise ValueError("%s: a row's heads must be contiguous" % name)
-    return st[0] if rows > 1 else heads * dim
+    return t.data_ptr(), (st[0] if rows > 1 else heads * dim)
 
 
-def _table(t, name: str = "table"):
-    """A page table [batch][columns]."""
-    _dev(t, torch.int32, name)
+def _table(t, name: str, dev: int):
+    """A page table [batch][columns]: (address, batch, columns)."""
+    p = _arg(t, torch.int32, name, 0, dev)
     if t.dim() != 2:
         raise ValueError("%s must be [batch][pages of a sequence]" % name)
-    return t.shape
+    batch, cols = t.shape
+    return p, batch, cols
 
 
 def _type(t, name: str, types) -> int:
@@ -511,73 +529,76 @@ def _type(t, name: str, types) -> int:
     return XP_TYPES[dt]
 
 
-def _on(first, *others):
-    """The device guard of a call: all its tensors lie on one device, which need not be the current one."""
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("tensors on %s and %s in one call" % (first.device, t.device))
-    return torch.cuda.device(first.device)
+_HALVES = (torch.bfloat16, torch.float16)
 
 
-def _cache(d: xp_kv_dims, cache) -> None:
-    _dev(cache, torch.uint8, "cache", xp_kv_bytes(d))
+def _weights(w, name: str, batch: int, kv_heads: int, least: int, dev: int):
+    """Accumulated weights fp32 [batch][kv_heads][columns], contiguous: (address, stride of a row)."""
+    p = _arg(w, torch.float32, name, 0, dev)
+    if w.dim() != 3 or w.shape[0] != batch or w.shape[1] != kv_heads or w.shape[2] < least:
+        raise ValueError("%s must be [%d, %d, at least %d], got %s" % (name, batch, kv_heads, least, list(w.shape)))
+    return p, w.shape[2]
+
+
+def _cache_bytes(d: xp_kv_dims) -> int:
+    return d.n_pages * d.kv_heads * (d.page // 64) * (d.head_dim // 32) * 2176
+
+
+def _launch(fn, where: str, dev: int, stream, args) -> None:
+    """Call fn on device dev (which need not be the current one), on `stream` or dev's current stream."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, int(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, int(stream))
+    if status != XP_OK:
+        raise XPError(status, where)
 
 
 def xp_kv_append(d: xp_kv_dims, k, v, cu_rows, start, table, cache, stream=None) -> None:
     """Quantise the packed rows k, v [rows][kv_heads][head_dim] into the cache (see xp.h)."""
-    ty = _type(k, "k", tuple(XP_TYPES))
-    batch, cols = _table(table)
+    ty, dev, heads, dim = _type(k, "k", XP_TYPES), k.get_device(), d.kv_heads, d.head_dim
+    tp, batch, cols = _table(table, "table", dev)
     rows = k.shape[0]
-    ks = _rows3(k, k.dtype, "k", rows, d.kv_heads, d.head_dim)
-    vs = _rows3(v, k.dtype, "v", rows, d.kv_heads, d.head_dim)
-    _dev(cu_rows, torch.int32, "cu_rows", batch + 1)
-    _dev(start, torch.int32, "start", batch)
-    _cache(d, cache)
-    with _on(cache, k, v, cu_rows, start, table):
-        _check(lib().xp_kv_append(ctypes.byref(d), batch, cols, rows, ty, _ptr(k), ks, _ptr(v), vs, _ptr(cu_rows),
-                                  _ptr(start), _ptr(table), _ptr(cache), _stream(stream)), "xp_kv_append")
+    kp, ks = _rows3(k, k.dtype, "k", rows, heads, dim, dev)
+    vp, vs = _rows3(v, k.dtype, "v", rows, heads, dim, dev)
+    _launch(lib().xp_kv_append, "xp_kv_append", dev, stream,
+            (ctypes.byref(d), batch, cols, rows, ty, kp, ks, vp, vs, _arg(cu_rows, torch.int32, "cu_rows", batch + 1, dev),
+             _arg(start, torch.int32, "start", batch, dev), tp, _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev)))
 
 
 def xp_kv_read(d: xp_kv_dims, cu_rows, start, table, cache, k, v, stream=None) -> None:
     """Read cached rows back into k, v [rows][kv_heads][head_dim] (see xp.h)."""
-    ty = _type(k, "k", tuple(XP_TYPES))
-    batch, cols = _table(table)
+    ty, dev, heads, dim = _type(k, "k", XP_TYPES), k.get_device(), d.kv_heads, d.head_dim
+    tp, batch, cols = _table(table, "table", dev)
     rows = k.shape[0]
-    ks = _rows3(k, k.dtype, "k", rows, d.kv_heads, d.head_dim)
-    vs = _rows3(v, k.dtype, "v", rows, d.kv_heads, d.head_dim)
-    _dev(cu_rows, torch.int32, "cu_rows", batch + 1)
-    _dev(start, torch.int32, "start", batch)
-    _cache(d, cache)
-    with _on(cache, k, v, cu_rows, start, table):
-        _check(lib().xp_kv_read(ctypes.byref(d), batch, cols, rows, ty, _ptr(cu_rows), _ptr(start), _ptr(table),
-                                _ptr(cache), _ptr(k), ks, _ptr(v), vs, _stream(stream)), "xp_kv_read")
-
-
-def _weights(w, name: str, batch: int, kv_heads: int, least: int) -> int:
-    """Accumulated weights fp32 [batch][kv_heads][columns], contiguous; the stride of a row."""
-    _dev(w, torch.float32, name)
-    if w.dim() != 3 or w.shape[0] != batch or w.shape[1] != kv_heads or w.shape[2] < least:
-        raise ValueError("%s must be [%d, %d, at least %d], got %s" % (name, batch, kv_heads, least, list(w.shape)))
-    return w.shape[2]
+    kp, ks = _rows3(k, k.dtype, "k", rows, heads, dim, dev)
+    vp, vs = _rows3(v, k.dtype, "v", rows, heads, dim, dev)
+    _launch(lib().xp_kv_read, "xp_kv_read", dev, stream,
+            (ctypes.byref(d), batch, cols, rows, ty, _arg(cu_rows, torch.int32, "cu_rows", batch + 1, dev),
+             _arg(start, torch.int32, "start", batch, dev), tp, _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev),
+             kp, ks, vp, vs))
 
 
 def xp_kv_evict(d: xp_kv_dims, cache, table, lens, weights, keep: int, dst_table, kept, lens_out, weights_out,
                 sinks: int = 0, recent: int = 0, stream=None) -> None:
     """Cut sequences to ``keep`` positions by accumulated weight (see xp.h)."""
-    batch, cols = _table(table)
-    dbatch, dcols = _table(dst_table, "dst_table")
+    keep, i32 = int(keep), torch.int32
+    dev = cache.get_device() if isinstance(cache, torch.Tensor) else -1
+    tp, batch, cols = _table(table, "table", dev)
+    dp, dbatch, dcols = _table(dst_table, "dst_table", dev)
     if dbatch != batch:
         raise ValueError("dst_table has %d sequences, table %d" % (dbatch, batch))
-    ws = _weights(weights, "weights", batch, d.kv_heads, cols * d.page)
-    wo = _weights(weights_out, "weights_out", batch, d.kv_heads, int(keep))
-    _dev(lens, torch.int32, "lens", batch)
-    _dev(lens_out, torch.int32, "lens_out", batch)
-    _dev(kept, torch.int32, "kept", batch * d.kv_heads * int(keep))
-    _cache(d, cache)
-    with _on(cache, table, lens, weights, dst_table, kept, lens_out, weights_out):
-        _check(lib().xp_kv_evict(ctypes.byref(d), batch, cols, _ptr(cache), _ptr(table), _ptr(lens), _ptr(weights), ws,
-                                 int(keep), int(sinks), int(recent), dcols, _ptr(dst_table), _ptr(kept),
-                                 _ptr(lens_out), _ptr(weights_out), wo, _stream(stream)), "xp_kv_evict")
+    wp, ws = _weights(weights, "weights", batch, d.kv_heads, cols * d.page, dev)
+    op, wo = _weights(weights_out, "weights_out", batch, d.kv_heads, keep, dev)
+    _launch(lib().xp_kv_evict, "xp_kv_evict", dev, stream,
+            (ctypes.byref(d), batch, cols, _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev), tp,
+             _arg(lens, i32, "lens", batch, dev), wp, ws, keep, int(sinks), int(recent), dcols, dp,
+             _arg(kept, i32, "kept", batch * d.kv_heads * keep, dev), _arg(lens_out, i32, "lens_out", batch, dev), op, wo))
 
 
 def xp_attn_decode_workspace_bytes(d: xp_kv_dims, heads: int, q_rows: int, batch: int, max_len: int) -> int:
@@ -588,42 +609,35 @@ def xp_attn_decode_workspace_bytes(d: xp_kv_dims, heads: int, q_rows: int, batch
 def xp_attn_decode(d: xp_kv_dims, q, cache, table, lens, max_len: int, scale: float, out, workspace, q_rows: int = 1,
                    window: int = 0, weights=None, stream=None) -> None:
     """Attention of q [batch * q_rows][heads][head_dim] over the 4-bit cache (see xp.h)."""
-    ty = _type(q, "q", (torch.bfloat16, torch.float16))
-    batch, cols = _table(table)
-    heads = q.shape[1] if q.dim() == 3 else 0
-    qs = _rows3(q, q.dtype, "q", batch * int(q_rows), heads, d.head_dim)
-    os_ = _rows3(out, q.dtype, "out", batch * int(q_rows), heads, d.head_dim)
-    _dev(lens, torch.int32, "lens", batch)
-    _dev(workspace, torch.uint8, "workspace")
-    _cache(d, cache)
-    ws = 0 if weights is None else _weights(weights, "weights", batch, d.kv_heads, cols * d.page)
-    with _on(cache, q, table, lens, out, workspace, weights):
-        _check(lib().xp_attn_decode(ctypes.byref(d), heads, int(q_rows), batch, cols, int(max_len), ty, _ptr(q), qs,
-                                    scale, int(window), _ptr(cache), _ptr(table), _ptr(lens), _ptr(out), os_,
-                                    _ptr(weights), ws, _ptr(workspace), workspace.numel(), _stream(stream)),
-               "xp_attn_decode")
+    ty, dev, q_rows = _type(q, "q", _HALVES), q.get_device(), int(q_rows)
+    tp, batch, cols = _table(table, "table", dev)
+    heads, dim = q.shape[1] if q.dim() == 3 else 0, d.head_dim
+    qp, qs = _rows3(q, q.dtype, "q", batch * q_rows, heads, dim, dev)
+    op, os_ = _rows3(out, q.dtype, "out", batch * q_rows, heads, dim, dev)
+    wp, ws = (0, 0) if weights is None else _weights(weights, "weights", batch, d.kv_heads, cols * d.page, dev)
+    _launch(lib().xp_attn_decode, "xp_attn_decode", dev, stream,
+            (ctypes.byref(d), heads, q_rows, batch, cols, int(max_len), ty, qp, qs, scale, int(window),
+             _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev), tp, _arg(lens, torch.int32, "lens", batch, dev), op,
+             os_, wp, ws, _arg(workspace, torch.uint8, "workspace", 0, dev), workspace.numel()))
 
 
 def xp_attn_prompt(q, k, v, cu_q, cu_k, scale: float, out, window: int = 0, stream=None) -> None:
     """Causal attention over packed prompts: q, out [rows_q][heads][head_dim], k, v
     [rows_k][kv_heads][head_dim] (see xp.h)."""
-    ty = _type(q, "q", (torch.bfloat16, torch.float16))
+    ty, dev = _type(q, "q", _HALVES), q.get_device()
     if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("q and k must be [rows][heads][head_dim]")
     rows_q, heads, dim = q.shape
-    rows_k, kv_heads = k.shape[0], k.shape[1]
-    qs = _rows3(q, q.dtype, "q", rows_q, heads, dim)
-    ks = _rows3(k, q.dtype, "k", rows_k, kv_heads, dim)
-    vs = _rows3(v, q.dtype, "v", rows_k, kv_heads, dim)
-    os_ = _rows3(out, q.dtype, "out", rows_q, heads, dim)
-    _dev(cu_q, torch.int32, "cu_q")
-    _dev(cu_k, torch.int32, "cu_k", cu_q.numel())
-    if cu_q.numel() < 1:
-        raise ValueError("cu_q must hold the ends of each sequence, from 0")
-    with _on(q, k, v, cu_q, cu_k, out):
-        _check(lib().xp_attn_prompt(heads, kv_heads, dim, cu_q.numel() - 1, rows_q, rows_k, ty, _ptr(q), qs, _ptr(k),
-                                    ks, _ptr(v), vs, _ptr(cu_q), _ptr(cu_k), scale, int(window), _ptr(out), os_,
-                                    _stream(stream)), "xp_attn_prompt")
+    rows_k, kv_heads, _ = k.shape
+    qp, qs = _rows3(q, q.dtype, "q", rows_q, heads, dim, dev)
+    kp, ks = _rows3(k, q.dtype, "k", rows_k, kv_heads, dim, dev)
+    vp, vs = _rows3(v, q.dtype, "v", rows_k, kv_heads, dim, dev)
+    op, os_ = _rows3(out, q.dtype, "out", rows_q, heads, dim, dev)
+    cq = _arg(cu_q, torch.int32, "cu_q", 1, dev)
+    seqs = cu_q.numel()
+    _launch(lib().xp_attn_prompt, "xp_attn_prompt", dev, stream,
+            (heads, kv_heads, dim, seqs - 1, rows_q, rows_k, ty, qp, qs, kp, ks, vp, vs, cq,
+             _arg(cu_k, torch.int32, "cu_k", seqs, dev), scale, int(window), op, os_))
 
 
 # -------------------------------------------------------------- conveniences
