@@ -229,14 +229,22 @@ __device__ __forceinline__ int length_of(const Args& a, int b) {
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
 
-__device__ __forceinline__ uint16_t to16(float f, bool bf16) {
-    return bf16 ? bf16_rne(f) : __builtin_bit_cast(uint16_t, (_Float16)f);
+// Four outputs to 16 bits, nearest even.
+template <bool BF16>
+__device__ __forceinline__ uint2 to16(f32x4 v) {
+    if constexpr (BF16) {
+        typedef __attribute__((ext_vector_type(4))) __bf16 b16x4;
+        return __builtin_bit_cast(uint2, __builtin_convertvector(v, b16x4));
+    } else {
+        typedef __attribute__((ext_vector_type(4))) _Float16 h16x4;
+        return __builtin_bit_cast(uint2, __builtin_convertvector(v, h16x4));
+    }
 }
 
 // One workgroup: a split of one (sequence, kv head, block of 16*MT rows); its four
 // waves take tiles in turn and join in LDS.
 template <int D, int MT, bool BF16>
-__global__ __launch_bounds__(256) void attn_decode_kernel(Args a) {
+__global__ __launch_bounds__(256, MT > 1 ? 1 : (D == 64 ? 4 : (D == 128 ? 3 : 2))) void attn_decode_kernel(Args a) {
     constexpr int NW = Dim<D>::NW, NG = Dim<D>::NG, NH = Dim<D>::NH, VD = Dim<D>::VD;
     constexpr int kRegion = Dim<D>::kVBytes + NG * 64;     // a wave's V codes and scales
     constexpr int kJoin = MT * NH * 64 * 16;               // one wave's output, fp32
@@ -279,15 +287,20 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(Args a) {
         for (int j = 0; j < (SW + 63) / 64; ++j)
             vs[j] = j * 64 + lane < SW ? *(const uint32_t*)(t + NG * 2112 + (j * 64 + lane) * 4) : 0u;
     };
-    // the next tile at or behind `tile` whose page exists (positions of others are not seen)
+    // the next tile at or behind `tile` whose page exists (positions of others are not seen);
+    // its page's column and its place on the page follow it
+    const int page_tiles = a.g.page >> 6;
+    const long long tile_bytes = kv::tile_bytes(NG);
+    int tile = t0 + wave, col = tile / page_tiles, in_page = tile - col * page_tiles;
     auto find = [&](int& tile) {
         for (; tile < t1; tile += kWaves) {
-            const long long at = kv::tile_at(a.g, tr, head, tile * 64);
-            if (at >= 0) return a.cache + at;
+            const int id = tr[col];
+            const long long at = (((long long)id * a.g.kv_heads + head) * page_tiles + in_page) * tile_bytes;
+            for (in_page += kWaves; in_page >= page_tiles; in_page -= page_tiles) ++col;
+            if ((unsigned)id < (unsigned)a.g.n_pages) return a.cache + at;
         }
         return a.cache;
     };
-    int tile = t0 + wave;
     const uint8_t* t = find(tile);
     if (tile < t1) {
         load_k<D>(k, t, c, q);
@@ -395,19 +408,39 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(Args a) {
             l[mt] += add;
         }
 
+        if (masked && nan_v) {
+            // a zero weight times a NaN scale is NaN: rows that see such a position get NaN in its
+            // group's columns here, and the scale leaves the tile
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint8_t* sb = region + Dim<D>::kVBytes + g * 64 + q * 16;
+                uint32_t bad = 0;
+#pragma unroll 1
+                for (int e = 0; e < 16; ++e) bad |= ((sb[e] & 127u) == 127u ? 1u : 0u) << e;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const Span sp = span_of(a, len, (rb * MT + mt) * 16 + c);
+                    float hit = 0.0f;
+#pragma unroll 1
+                    for (int e = 0; e < 16; ++e) {
+                        const int ps = tile * 64 + 16 * (e >> 2) + 4 * q + (e & 3);
+                        if ((bad >> e & 1u) && ps >= sp.lo && ps < sp.hi) hit = 1.0f;
+                    }
+                    const float add = max_over_q(hit) > 0.0f ? __builtin_nanf("") : 0.0f;
+                    o[mt][2 * g] += add;
+                    o[mt][2 * g + 1] += add;
+                }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+                for (int e = 0; e < 16; ++e)
+                    if (bad >> e & 1u) sb[e] = 0;
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const uint4 sc = *(const uint4*)(region + Dim<D>::kVBytes + g * 64 + q * 16);
-            uint32_t sd[4] = {sc.x, sc.y, sc.z, sc.w};
-            bool bad[16];
-            if (masked && nan_v) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint32_t byte = (sd[e >> 2] >> (8 * (e & 3))) & 127u;
-                    bad[e] = byte == 127u;
-                    if (bad[e]) sd[e >> 2] &= ~(255u << (8 * (e & 3)));
-                }
-            }
+            const uint32_t sd[4] = {sc.x, sc.y, sc.z, sc.w};
             h16x2 sv[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -426,23 +459,6 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(Args a) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
                         o[mt][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[mt][st], o[mt][h], 0, 0, 0);
-                }
-            }
-            if (masked && nan_v) {
-                // rows that see a position whose scale is NaN hold NaN in this group's columns
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const Span sp = span_of(a, len, (rb * MT + mt) * 16 + c);
-                    float hit = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int ps = tile * 64 + 16 * (e >> 2) + 4 * q + (e & 3);
-                        if (bad[e] && ps >= sp.lo && ps < sp.hi) hit = 1.0f;
-                    }
-                    if (max_over_q(hit) > 0.0f) {
-                        o[mt][2 * g] = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
-                        o[mt][2 * g + 1] = o[mt][2 * g];
-                    }
                 }
             }
         }
@@ -507,11 +523,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(Args a) {
         const float inv = l[mt] == 0.0f ? 0.0f : 1.0f / l[mt];    // nothing seen: zeros
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            const f32x4 v = o[mt][h] * inv;
-            uint2 w;
-            w.x = (uint32_t)to16(v[0], BF16) | (uint32_t)to16(v[1], BF16) << 16;
-            w.y = (uint32_t)to16(v[2], BF16) | (uint32_t)to16(v[3], BF16) << 16;
-            *(uint2*)(y + 16 * h + 4 * q) = w;
+            *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(o[mt][h] * inv);
         }
         if (a.lse && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
             l[mt] == 0.0f ? __builtin_inff() : (m[mt] - kLift) + __builtin_amdgcn_logf(l[mt]);
@@ -579,11 +591,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int tok = r / a.group, hd = head * a.group + r - tok * a.group;
     uint16_t* y = (uint16_t*)a.out + ((long long)b * a.q_rows + tok) * a.out_stride + (long long)hd * D;
-    const f32x4 v = o * inv;
-    uint2 w;
-    w.x = (uint32_t)to16(v[0], BF16) | (uint32_t)to16(v[1], BF16) << 16;
-    w.y = (uint32_t)to16(v[2], BF16) | (uint32_t)to16(v[3], BF16) << 16;
-    *(uint2*)(y + 16 * h + 4 * q) = w;
+    *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(o * inv);
     if (a.lse && h == 0 && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
         l == 0.0f ? __builtin_inff() : (m - kLift) + __builtin_amdgcn_logf(l);
 }
