@@ -30,7 +30,6 @@ typedef __attribute__((ext_vector_type(8))) _Float16 h16x8;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(2))) int i32x2;
 
-constexpr int kWaves = 4;
 constexpr float kLift = 15.0f;   // exponentials are held as 2^kLift p: 2^15 is fp16's largest power of two
 
 struct Args {
@@ -42,13 +41,15 @@ struct Args {
     const int32_t* lens;
     void* out;
     long long out_stride;
-    float* part;          // partial outputs of the splits, unscaled
+    float* part;          // partial outputs of cut sequences' pieces, unscaled
     float* part_ml;       // their maxima and sums
     float* lse;           // per row: the maximum in log2 units and the sum's logarithm, for the weights
     float* weights;
     long long w_stride;
     int heads, group, q_rows, row_blocks, window;
-    int splits, chunk;    // a split is `chunk` tiles; the last one takes what is left
+    int batch;
+    int share, chunk;     // sequences longer than max(tiles of the batch / share, chunk) tiles are cut into pieces
+    int waves;            // of a workgroup; pieces are whole rounds of them
     float scale_m;        // scale * log2(e) = scale_m * 2^scale_e
     int scale_e;
 };
@@ -210,23 +211,170 @@ __device__ __forceinline__ Span span_of(const Args& a, int len, int r) {
 struct Tiles {
     int lo, hi;
 };
-__device__ __forceinline__ Tiles tiles_of(const Args& a, const Span& first, const Span& last) {
+__device__ __forceinline__ Tiles tiles_of(const Args& a, int len, int first_row, int last_row) {
+    const Span first = span_of(a, len, first_row), last = span_of(a, len, last_row);
     Tiles t;
     t.lo = first.lo >> 6;
     t.hi = last.hi > 0 ? (last.hi + 63) >> 6 : 0;
     if (t.hi < t.lo) t.hi = t.lo;
     return t;
 }
-template <int MT>
-__device__ __forceinline__ int last_row(const Args& a, int rb) {
-    const int rows = a.q_rows * a.group, end = (rb + 1) * MT * 16;
-    return (end < rows ? end : rows) - 1;
-}
 
 __device__ __forceinline__ int length_of(const Args& a, int b) {
     const int cap = a.g.max_pages * a.g.page;
     const int n = a.lens[b];
     return n < 0 ? 0 : (n > cap ? cap : n);
+}
+
+// The pieces of a launch. A unit is a (sequence, kv head, row block); a sequence's
+// units are cut alike, into pieces that no more than one of `share` workgroups' even
+// share of all tiles makes long, and sequences that are short enough are left whole.
+// Cut sequences come first, then the whole ones, in batches of up to 64 the longer
+// ones first, so that the short ones fill the gaps at the end. There are at
+// most 2 * share pieces of cut sequences and share + units pieces in all.
+struct Piece {
+    int b, unit;          // sequence; kv head + kv_heads * row block
+    int pieces, slot;     // pieces of the sequence; place of this unit's first one, kv_heads * row_blocks apart
+    int tiles, lo, each;  // tiles of the sequence, the first one, tiles of a piece
+    int index;            // which piece
+    int len;
+};
+struct Cut {
+    int tiles, lo, pieces, each;
+};
+__device__ __forceinline__ Cut cut_of(const Args& a, int len, int limit) {
+    const Tiles t = tiles_of(a, len, 0, a.q_rows * a.group - 1);
+    Cut c;
+    c.lo = t.lo;
+    c.tiles = t.hi - t.lo;
+    c.pieces = c.tiles > limit ? (c.tiles + limit - 1) / limit : 1;
+    c.each = (c.tiles + c.pieces - 1) / c.pieces;
+    return c;
+}
+__device__ __forceinline__ int limit_of(const Args& a, long long even) {
+    const int n = even > a.chunk ? (even > (1 << 26) ? 1 << 26 : (int)even) : a.chunk;
+    return (n + a.waves - 1) / a.waves * a.waves;
+}
+// Piece i of the launch (JOIN: unit i of the cut sequences); false: there is none.
+template <bool JOIN>
+__device__ __forceinline__ bool find_piece(const Args& a, int i, Piece& p) {
+    const int lane = threadIdx.x & 63, per = a.g.kv_heads * a.row_blocks;
+    int limit = 0x7fffffff, len = 0;
+    // a sequence's last piece is half empty on average: keep the pieces within one for each workgroup
+    const long long units = (long long)a.batch * per, share = a.share - (units < a.share ? units : a.share) / 2;
+    Cut c{};
+    if (a.batch <= 64) {
+        const bool in = lane < a.batch;
+        len = in ? length_of(a, lane) : 0;
+        c = cut_of(a, len, limit);
+        if (a.share) {
+            const int sum = wave_incl_sum(in ? c.tiles : 0);
+            const long long all = (long long)(uint32_t)__builtin_amdgcn_readlane(sum, 63) * per;   // 64 * 2^25 tiles at most
+            const long long even = (all + share - 1) / share;
+            limit = limit_of(a, even);
+            if (__ballot(in && c.tiles > limit)) c = cut_of(a, len, limit);
+        }
+        const bool is_cut = in && c.pieces > 1;
+        const uint64_t cuts = __ballot(is_cut);
+        int from = 0, first = 0;                           // pieces before this sequence's; (JOIN) units
+        if (cuts) {
+            first = wave_incl_sum(is_cut ? c.pieces * per : 0);
+            from = __builtin_amdgcn_readlane(first, 63);
+            first -= is_cut ? c.pieces * per : 0;
+        }
+        uint64_t hit;
+        if (JOIN) {
+            const int j = __popcll(cuts & ((1ull << lane) - 1)) * per;
+            hit = __ballot(is_cut && j <= i && i < j + per);
+            i -= j;                                        // per lane: read back from the one that hit
+        } else {
+            if (i >= from + (a.batch - __popcll(cuts)) * per) return false;
+            if (i < from) {
+                hit = __ballot(is_cut && first <= i && i < first + c.pieces * per);
+                i -= first;
+            } else {
+                // eight classes of length, the longest first
+                const int top = (int)wave_max_u32(in && !is_cut ? (uint32_t)c.tiles : 0u);
+                const int cls = in && !is_cut ? (top > 0 ? (int)(8.0f * (float)c.tiles / (float)(top + 1)) : 0) : -1;
+                int before = 0;
+#pragma unroll
+                for (int k = 7; k >= 0; --k) {
+                    const uint64_t same = __ballot(cls == k);
+                    if (cls > k) continue;
+                    before += __popcll(cls == k ? same & ((1ull << lane) - 1) : same);
+                }
+                first = from + before * per;
+                hit = __ballot(cls >= 0 && first <= i && i < first + per);
+                i -= first;
+            }
+        }
+        if (!hit) return false;
+        const int l = __ffsll((unsigned long long)hit) - 1;
+        p.b = l;
+        const int at = __builtin_amdgcn_readlane(i, l);
+        p.index = JOIN ? 0 : at / per;
+        p.unit = at - p.index * per;
+        p.pieces = __builtin_amdgcn_readlane(c.pieces, l);
+        p.slot = __builtin_amdgcn_readlane(first, l) + p.unit;
+        p.tiles = __builtin_amdgcn_readlane(c.tiles, l);
+        p.lo = __builtin_amdgcn_readlane(c.lo, l);
+        p.each = __builtin_amdgcn_readlane(c.each, l);
+        p.len = __builtin_amdgcn_readlane(len, l);
+        return true;
+    }
+    // more sequences: their order is kept inside the cut and the whole ones
+    if (!a.share) {
+        if (JOIN || i >= (long long)a.batch * per) return false;
+        p.b = i / per;
+        p.unit = i - p.b * per;
+        p.len = length_of(a, p.b);
+        c = cut_of(a, p.len, limit);
+        p.pieces = 1;
+        p.slot = i;
+        p.tiles = p.each = c.tiles;
+        p.lo = c.lo;
+        p.index = 0;
+        return true;
+    }
+    {
+        long long all = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 64) {
+            c = cut_of(a, b0 + lane < a.batch ? length_of(a, b0 + lane) : 0, limit);
+            const int v = wave_incl_sum(b0 + lane < a.batch ? c.tiles : 0);
+            all += (uint32_t)__builtin_amdgcn_readlane(v, 63);
+        }
+        const long long even = (all * per + share - 1) / share;
+        limit = limit_of(a, even);
+    }
+    int start = 0, jstart = 0;
+    for (int whole = 0; whole < (JOIN ? 1 : 2); ++whole)
+        for (int b0 = 0; b0 < a.batch; b0 += 64) {
+            const bool in = b0 + lane < a.batch;
+            len = in ? length_of(a, b0 + lane) : 0;
+            c = cut_of(a, len, limit);
+            const bool sel = in && (c.pieces == 1) == (whole == 1);
+            const int mine = sel ? c.pieces * per : 0, joins = sel ? per : 0;
+            const int incl = wave_incl_sum(mine), jincl = wave_incl_sum(joins);
+            const int from = JOIN ? jstart + jincl - joins : start + incl - mine, n = JOIN ? joins : mine;
+            const uint64_t hit = __ballot(sel && from <= i && i < from + n);
+            if (hit) {
+                const int l = __ffsll((unsigned long long)hit) - 1;
+                p.b = b0 + l;
+                const int at = i - __builtin_amdgcn_readlane(from, l);
+                p.index = JOIN ? 0 : at / per;
+                p.unit = at - p.index * per;
+                p.pieces = __builtin_amdgcn_readlane(c.pieces, l);
+                p.slot = start + __builtin_amdgcn_readlane(incl - mine, l) + p.unit;
+                p.tiles = __builtin_amdgcn_readlane(c.tiles, l);
+                p.lo = __builtin_amdgcn_readlane(c.lo, l);
+                p.each = __builtin_amdgcn_readlane(c.each, l);
+                p.len = __builtin_amdgcn_readlane(len, l);
+                return true;
+            }
+            start += __builtin_amdgcn_readlane(incl, 63);
+            jstart += __builtin_amdgcn_readlane(jincl, 63);
+        }
+    return false;
 }
 
 // Four outputs to 16 bits, nearest even.
@@ -241,33 +389,44 @@ __device__ __forceinline__ uint2 to16(f32x4 v) {
     }
 }
 
-// One workgroup: a split of one (sequence, kv head, block of 16*MT rows); its four
-// waves take tiles in turn and join in LDS.
+// Waves a CU holds at once, by registers: also the most a workgroup takes.
+template <int D, int MT>
+constexpr int waves_per_cu() {
+    return MT == 1 ? (D == 64 ? 16 : (D == 128 ? 12 : 8)) : (D == 64 ? 8 : 4);
+}
+template <int D, int MT>
+constexpr int region_bytes() {
+    return Dim<D>::kVBytes + Dim<D>::NG * 64;              // a wave's V codes and scales
+}
+template <int D, int MT>
+constexpr int join_bytes() {
+    return MT * Dim<D>::NH * 1024 + MT * 128;              // a wave's output, maxima and sums
+}
+
+// One workgroup: a split of one (sequence, kv head, block of 16*MT rows); its waves
+// take tiles in turn and join in LDS.
 template <int D, int MT, bool BF16>
-__global__ __launch_bounds__(256, MT > 1 ? 1 : (D == 64 ? 4 : (D == 128 ? 3 : 2))) void attn_decode_kernel(Args a) {
+__global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kernel(Args a) {
     constexpr int NW = Dim<D>::NW, NG = Dim<D>::NG, NH = Dim<D>::NH, VD = Dim<D>::VD;
-    constexpr int kRegion = Dim<D>::kVBytes + NG * 64;     // a wave's V codes and scales
-    constexpr int kJoin = MT * NH * 64 * 16;               // one wave's output, fp32
-    constexpr int kLds = kWaves * kRegion > 2 * kJoin ? kWaves * kRegion : 2 * kJoin;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
-    __shared__ float join_ml[2][2][MT * 64];
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int head = blockIdx.y % a.g.kv_heads, rb = blockIdx.y / a.g.kv_heads, b = blockIdx.z;
-    const int len = length_of(a, b);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    Piece pc;
+    if (!find_piece<false>(a, blockIdx.x, pc)) return;
+    const int b = pc.b, len = pc.len, rb = pc.unit / a.g.kv_heads, head = pc.unit - rb * a.g.kv_heads;
     const int32_t* tr = a.table + (long long)b * a.g.max_pages;
 
-    // this block's tiles: those that its rows see
-    const int rows = a.q_rows * a.group;
-    const Span s_first = span_of(a, len, rb * MT * 16), s_last = span_of(a, len, last_row<MT>(a, rb));
-    const Tiles tl = tiles_of(a, s_first, s_last);
-    const int t0 = tl.lo + (int)blockIdx.x * a.chunk;
-    if (blockIdx.x > 0 && t0 >= tl.hi) return;
-    const int t1 = (int)blockIdx.x == a.splits - 1 || t0 + a.chunk > tl.hi ? tl.hi : t0 + a.chunk;
-    const bool whole = t1 == tl.hi && blockIdx.x == 0;     // nothing to join
-    // tiles that every row sees whole
-    const int full_lo = s_last.lo, full_hi = s_first.hi;
+    // this piece's tiles, less those that no row of the block sees
+    const int rows = a.q_rows * a.group, first_row = rb * MT * 16;
+    const int last_row = first_row + MT * 16 < rows ? first_row + MT * 16 - 1 : rows - 1;
+    const Tiles tl = tiles_of(a, len, first_row, last_row);
+    int t0 = pc.lo + pc.index * pc.each, t1 = t0 + pc.each;
+    t1 = t1 > pc.lo + pc.tiles ? pc.lo + pc.tiles : t1;
+    t0 = t0 < tl.lo ? tl.lo : t0;
+    t1 = t1 > tl.hi ? tl.hi : t1;
+    // positions that every row sees
+    const int full_lo = span_of(a, len, last_row).lo, full_hi = span_of(a, len, first_row).hi;
 
     // a tile's bytes, loaded one tile ahead: K once its scores are formed, V once it is in LDS
     KTile<D> k;
@@ -293,10 +452,10 @@ __global__ __launch_bounds__(256, MT > 1 ? 1 : (D == 64 ? 4 : (D == 128 ? 3 : 2)
     const long long tile_bytes = kv::tile_bytes(NG);
     int tile = t0 + wave, col = tile / page_tiles, in_page = tile - col * page_tiles;
     auto find = [&](int& tile) {
-        for (; tile < t1; tile += kWaves) {
+        for (; tile < t1; tile += waves) {
             const int id = tr[col];
             const long long at = (((long long)id * a.g.kv_heads + head) * page_tiles + in_page) * tile_bytes;
-            for (in_page += kWaves; in_page >= page_tiles; in_page -= page_tiles) ++col;
+            for (in_page += waves; in_page >= page_tiles; in_page -= page_tiles) ++col;
             if ((unsigned)id < (unsigned)a.g.n_pages) return a.cache + at;
         }
         return a.cache;
@@ -319,10 +478,10 @@ __global__ __launch_bounds__(256, MT > 1 ? 1 : (D == 64 ? 4 : (D == 128 ? 3 : 2)
 #pragma unroll
         for (int h = 0; h < NH; ++h) o[mt][h] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    uint8_t* region = lds + wave * kRegion;
+    uint8_t* region = lds + wave * region_bytes<D, MT>();
 
     while (tile < t1) {
-        int next = tile + kWaves;
+        int next = tile + waves;
         const uint8_t* nt = find(next);
         f32x4 s[MT][4];
 #pragma unroll
@@ -465,75 +624,62 @@ __global__ __launch_bounds__(256, MT > 1 ? 1 : (D == 64 ? 4 : (D == 128 ? 3 : 2)
         tile = next;
     }
 
-    // join the four waves: 2 and 3 into 0 and 1, then 1 into 0
+    // join the waves: each leaves its share in LDS, then takes every waves-th column block
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) l[mt] = sum_over_q(l[mt]);
-#pragma unroll
-    for (int half = 2; half >= 1; half >>= 1) {
-        __syncthreads();
-        if (wave >= half && wave < 2 * half) {
-            f32x4* buf = (f32x4*)(lds + (wave - half) * kJoin);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int h = 0; h < NH; ++h) buf[(mt * NH + h) * 64 + lane] = o[mt][h];
-                join_ml[wave - half][0][mt * 64 + lane] = m[mt];
-                join_ml[wave - half][1][mt * 64 + lane] = l[mt];
-            }
-        }
-        __syncthreads();
-        if (wave < half) {
-            const f32x4* buf = (const f32x4*)(lds + wave * kJoin);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const float om = join_ml[wave][0][mt * 64 + lane], ol = join_ml[wave][1][mt * 64 + lane];
-                const float nm = fmaxf(m[mt], om);
-                const float safe = nm == -__builtin_inff() ? 0.0f : nm;
-                const float fa = __builtin_amdgcn_exp2f(m[mt] - safe), fb = __builtin_amdgcn_exp2f(om - safe);
-                m[mt] = nm;
-                l[mt] = l[mt] * fa + ol * fb;
-#pragma unroll
-                for (int h = 0; h < NH; ++h) o[mt][h] = o[mt][h] * fa + buf[(mt * NH + h) * 64 + lane] * fb;
-            }
-        }
-    }
-    if (wave != 0) return;
-
-    const long long blk = ((long long)b * a.g.kv_heads + head) * a.row_blocks + rb;
-    if (!whole) {
-        f32x4* po = (f32x4*)a.part + (blk * a.splits + blockIdx.x) * (MT * NH * 64);
-        float* pm = a.part_ml + (blk * a.splits + blockIdx.x) * (MT * 32);
+    __syncthreads();                                       // the regions are read
+    {
+        f32x4* buf = (f32x4*)(lds + wave * join_bytes<D, MT>());
+        float* ml = (float*)(buf + MT * NH * 64);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-            for (int h = 0; h < NH; ++h) po[(mt * NH + h) * 64 + lane] = o[mt][h];
+            for (int h = 0; h < NH; ++h) buf[(mt * NH + h) * 64 + lane] = o[mt][h];
             if (q == 0) {
-                pm[mt * 32 + c] = m[mt];
-                pm[mt * 32 + 16 + c] = l[mt];
+                ml[mt * 32 + c] = m[mt];
+                ml[mt * 32 + 16 + c] = l[mt];
             }
         }
-        return;
     }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    __syncthreads();
+    const long long slot = pc.slot + (long long)pc.index * (a.g.kv_heads * a.row_blocks);
+    for (int col_block = wave; col_block < MT * NH; col_block += waves) {
+        const int mt = MT == 1 ? 0 : col_block / NH, h = col_block - mt * NH;
+        float jm = -__builtin_inff(), jl = 0.0f;
+        for (int w = 0; w < waves; ++w)
+            jm = fmaxf(jm, ((const float*)(lds + w * join_bytes<D, MT>() + MT * NH * 1024))[mt * 32 + c]);
+        const float safe = jm == -__builtin_inff() ? 0.0f : jm;
+        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int w = 0; w < waves; ++w) {
+            const uint8_t* from = lds + w * join_bytes<D, MT>();
+            const float* ml = (const float*)(from + MT * NH * 1024) + mt * 32 + c;
+            const float f = __builtin_amdgcn_exp2f(ml[0] - safe);
+            jl = __builtin_fmaf(ml[16], f, jl);
+            acc += ((const f32x4*)from)[col_block * 64 + lane] * f;
+        }
+        if (pc.pieces > 1) {
+            ((f32x4*)a.part)[(slot * (MT * NH) + col_block) * 64 + lane] = acc;
+            float* pm = a.part_ml + slot * (MT * 32);
+            if (h == 0 && q == 0) {
+                pm[mt * 32 + c] = jm;
+                pm[mt * 32 + 16 + c] = jl;
+            }
+            continue;
+        }
         const int r = (rb * MT + mt) * 16 + c;
         if (r >= rows) continue;
         const int tok = r / a.group, hd = head * a.group + r - tok * a.group;
         uint16_t* y = (uint16_t*)a.out + ((long long)b * a.q_rows + tok) * a.out_stride + (long long)hd * D;
-        const float inv = l[mt] == 0.0f ? 0.0f : 1.0f / l[mt];    // nothing seen: zeros
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(o[mt][h] * inv);
-        }
-        if (a.lse && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
-            l[mt] == 0.0f ? __builtin_inff() : (m[mt] - kLift) + __builtin_amdgcn_logf(l[mt]);
+        const float inv = jl == 0.0f ? 0.0f : 1.0f / jl;   // nothing seen: zeros
+        *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(acc * inv);
+        if (a.lse && h == 0 && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
+            jl == 0.0f ? __builtin_inff() : (jm - kLift) + __builtin_amdgcn_logf(jl);
     }
 }
 
-// Joins the splits: a workgroup takes four columns of 16 rows a lane, its waves take
-// the splits in turn (their partial outputs are 1 KiB loads that do not wait for each
-// other) and meet in LDS, in order. One wave over 256 splits took 130 us at one
-// sequence of 131,072 positions, the attention itself 19 us.
+// Joins the pieces of a cut sequence: a workgroup takes four columns of 16 rows a lane,
+// its waves take the pieces in turn (their partial outputs are 1 KiB loads that do not
+// wait for each other) and meet in LDS, in order.
 constexpr int kJoinWaves = 16;
 template <int D, int MT, bool BF16>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
@@ -543,15 +689,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int h = blockIdx.x % NH, mt = blockIdx.x / NH;
-    const int head = blockIdx.y % a.g.kv_heads, rb = blockIdx.y / a.g.kv_heads, b = blockIdx.z;
-    const int len = length_of(a, b);
-    const Tiles tl = tiles_of(a, span_of(a, len, rb * MT * 16), span_of(a, len, last_row<MT>(a, rb)));
-    int n = (tl.hi - tl.lo + a.chunk - 1) / a.chunk;
-    n = n < a.splits ? n : a.splits;
-    if (n <= 1) return;                                    // written by its only split
-    const long long blk = ((long long)b * a.g.kv_heads + head) * a.row_blocks + rb;
-    const f32x4* po = (const f32x4*)a.part + blk * a.splits * (MT * NH * 64) + blockIdx.x * 64 + lane;
-    const float* pm = a.part_ml + blk * a.splits * (MT * 32) + mt * 32 + c;
+    Piece pc;
+    if (!find_piece<true>(a, blockIdx.y, pc)) return;
+    const int b = pc.b, rb = pc.unit / a.g.kv_heads, head = pc.unit - rb * a.g.kv_heads, n = pc.pieces;
+    const long long step = a.g.kv_heads * a.row_blocks;    // slots from one piece of a unit to its next
+    const f32x4* po = (const f32x4*)a.part + (long long)pc.slot * (MT * NH * 64) + blockIdx.x * 64 + lane;
+    const float* pm = a.part_ml + (long long)pc.slot * (MT * 32) + mt * 32 + c;
     float m = -__builtin_inff(), l = 0.0f;
     f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
     constexpr int U = 8;
@@ -561,9 +704,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * waves < n ? s0 + u * waves : s0;
-            v[u] = po[(long long)s * (MT * NH * 64)];
-            vm[u] = pm[s * MT * 32];
-            vl[u] = pm[s * MT * 32 + 16];
+            v[u] = po[s * step * (MT * NH * 64)];
+            vm[u] = pm[s * step * (MT * 32)];
+            vl[u] = pm[s * step * (MT * 32) + 16];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -613,7 +756,7 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
     const int t_lo = span_of(a, len, 0).lo >> 6, t_hi = (len + 63) >> 6;
     const float* lse = a.lse + ((long long)b * a.heads + head * a.group) * a.q_rows;
     float* weights = a.weights + ((long long)b * a.g.kv_heads + head) * a.w_stride;
-    for (int tile = t_lo + blockIdx.x * kWaves + wave; tile < t_hi; tile += gridDim.x * kWaves) {
+    for (int tile = t_lo + blockIdx.x * 4 + wave; tile < t_hi; tile += gridDim.x * 4) {
         const long long at = kv::tile_at(a.g, tr, head, tile * 64);
         if (at < 0) continue;
         KTile<D> k;
@@ -656,35 +799,46 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
     }
 }
 
-// Rows of a block: 16 * MT. Sixty-four rows of 256 dims would need more registers than a wave has.
-static int row_tiles(int rows, int dim) { return rows <= 16 ? 1 : (rows <= 32 || dim == 256 ? 2 : 4); }
+// Rows of a block: 16 * MT.
+static int row_tiles(int rows, int dim) { return rows <= 16 || dim == 256 ? 1 : 2; }
 
-// Tiles of a split: about 1,536 splits in all where every sequence is as long as the
-// longest (six for each of the 256 CUs, so that shorter ones still leave the chip
-// full), but no fewer than two tiles for each of a workgroup's four waves.
-static int chunk_of(long long blocks, long long tiles) {
-    long long c = (blocks * tiles + 1535) / 1536;
-    c = (c + kWaves - 1) / kWaves * kWaves;
-    c = c < 2 * kWaves ? 2 * kWaves : c;
-    return (int)(c > (1 << 26) ? (1 << 26) : c);
-}
+constexpr int kCus = 256;
+// With two units a CU or more, sequences of up to this many tiles are never cut.
+constexpr int kLongTiles = 256;
 
 struct Launch {
-    int mt, row_blocks, splits, chunk;
+    int mt, row_blocks, waves, share, chunk, join_waves;
+    long long units;
     size_t part, ml, lse, total;
 };
-// What a call with these arguments launches and keeps in its workspace. A window does
-// not enter: the workspace is asked for without one.
-static Launch plan_of(const xp_kv_dims* d, int heads, int q_rows, int batch, int max_len) {
+// What a call with these arguments launches and keeps in its workspace (with a window
+// no more than without: it only shortens what is seen).
+static Launch plan_of(const xp_kv_dims* d, int heads, int q_rows, int batch, int max_len, int window) {
     Launch p{};
     const long long rows = (long long)q_rows * (heads / d->kv_heads);
     p.mt = row_tiles(rows > 64 ? 64 : (int)rows, d->head_dim);
     p.row_blocks = (int)((rows + 16 * p.mt - 1) / (16 * p.mt));
-    const long long blocks = (long long)batch * d->kv_heads * p.row_blocks;
-    const long long tiles = max_len < 1 ? 1 : ((long long)max_len + 63) / 64;
-    p.chunk = chunk_of(blocks < 1 ? 1 : blocks, tiles);
-    p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
-    const size_t parts = p.splits > 1 ? (size_t)blocks * p.splits : 0;
+    long long blocks = (long long)batch * d->kv_heads * p.row_blocks;
+    blocks = blocks < 1 ? 1 : blocks;
+    long long tiles = max_len < 1 ? 1 : ((long long)max_len + 63) / 64;
+    const long long seen = ((long long)window + q_rows + 62) / 64 + 1;
+    tiles = window > 0 && seen < tiles ? seen : tiles;
+    p.units = blocks;
+    const int most = d->head_dim == 64 ? (p.mt == 1 ? waves_per_cu<64, 1>() : waves_per_cu<64, 2>())
+                     : d->head_dim == 128 ? (p.mt == 1 ? waves_per_cu<128, 1>() : waves_per_cu<128, 2>())
+                                          : waves_per_cu<256, 1>();
+    // Contexts of a few rounds are left whole, by as many waves as there is room for. Longer
+    // ones are cut into one workgroup of the most waves on each CU where there are few units
+    // (one sequence of 131,072 positions, 4 kv heads: 24 us, against 28 in fours: fewer pieces
+    // to join), else into workgroups of four waves, as many as it holds (8 ragged sequences to
+    // 16,384, 8 kv heads, with weights: 54 us, against 65).
+    const bool many = blocks >= 2 * kCus, few = blocks <= 16, cut = tiles > (many ? kLongTiles : 3 * most);
+    p.waves = many || (cut && !few) ? 4 : (int)(tiles < most ? tiles : most);
+    p.chunk = many ? kLongTiles : 2 * p.waves;
+    p.share = cut ? kCus * (few ? 1 : most / 4) : 0;          // 0: no sequence is cut
+    const long long pieces = (tiles + p.chunk - 1) / p.chunk;
+    p.join_waves = (int)(pieces > 4 * kJoinWaves ? kJoinWaves : (pieces + 3) / 4);
+    const size_t parts = 2 * (size_t)p.share;
     p.part = 0;
     p.ml = parts * 16 * p.mt * d->head_dim * sizeof(float);
     p.lse = p.ml + align256(parts * 32 * p.mt * sizeof(float));
@@ -696,35 +850,32 @@ static int check_decode(const xp_kv_dims* d, int heads, int q_rows, int batch, i
     const int st = kv::check_geo(d, batch, max_pages);
     if (st != XP_OK) return st;
     if (heads < 1 || heads > 65535 || heads % d->kv_heads || q_rows < 1 || q_rows > 65535 || max_len < 0) return XP_ERR_SHAPE;
-    const Launch p = plan_of(d, heads, q_rows, batch, max_len);
-    if ((long long)p.row_blocks * d->kv_heads > 65535) return XP_ERR_SHAPE;
+    const Launch p = plan_of(d, heads, q_rows, batch, max_len, 0);
+    if (p.units + p.share > 0x7fffffffLL) return XP_ERR_SHAPE;
     return XP_OK;
 }
 
 template <int D, bool BF16>
 static int launch(const Args& a, const Launch& p, int batch, int max_len, hipStream_t s) {
-    const dim3 grid(p.splits, p.row_blocks * a.g.kv_heads, batch), block(256);
-    const dim3 join(p.mt * D / 16, grid.y, batch);
-    const int jw = (p.splits + 7) / 8;
-    const dim3 join_block(64 * (jw < kJoinWaves ? jw : kJoinWaves));
+    const dim3 grid((unsigned)(p.units + p.share)), block(64 * p.waves);
+    const dim3 join(p.mt * D / 16, (unsigned)(p.units < p.share ? p.units : p.share)), join_block(64 * p.join_waves);
 #define XP_ATTN_LAUNCH(MT_)                                                                        \
     do {                                                                                           \
-        hipLaunchKernelGGL((attn_decode_kernel<D, MT_, BF16>), grid, block, 0, s, a);              \
-        if (p.splits > 1) hipLaunchKernelGGL((attn_join_kernel<D, MT_, BF16>), join, join_block, 0, s, a); \
+        const int per_wave = join_bytes<D, MT_>() > region_bytes<D, MT_>() ? join_bytes<D, MT_>() : region_bytes<D, MT_>(); \
+        hipLaunchKernelGGL((attn_decode_kernel<D, MT_, BF16>), grid, block, p.waves * per_wave, s, a); \
+        if (p.share) hipLaunchKernelGGL((attn_join_kernel<D, MT_, BF16>), join, join_block, 0, s, a); \
     } while (0)
     if (p.mt == 1)
         XP_ATTN_LAUNCH(1);
-    else if (p.mt == 2)
-        XP_ATTN_LAUNCH(2);
     else if constexpr (D != 256)
-        XP_ATTN_LAUNCH(4);
+        XP_ATTN_LAUNCH(2);
 #undef XP_ATTN_LAUNCH
     int rc = launch_status();
     if (rc != XP_OK || !a.weights) return rc;
     const long long tiles = ((long long)max_len + 63) / 64;
-    long long blocks = (tiles + 2 * kWaves - 1) / (2 * kWaves);
+    long long blocks = (tiles + 7) / 8;
     blocks = blocks < 1 ? 1 : (blocks > 1024 ? 1024 : blocks);
-    hipLaunchKernelGGL((attn_weights_kernel<D, BF16>), dim3((unsigned)blocks, a.g.kv_heads, batch), block, 0, s, a);
+    hipLaunchKernelGGL((attn_weights_kernel<D, BF16>), dim3((unsigned)blocks, a.g.kv_heads, batch), dim3(256), 0, s, a);
     return launch_status();
 }
 
@@ -737,7 +888,7 @@ using namespace xp::attn;
 XP_API size_t xp_attn_decode_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_t batch,
                                              int32_t max_len) {
     if (check_decode(dims, heads, q_rows, batch, 1, max_len) != XP_OK) return 0;
-    return plan_of(dims, heads, q_rows, batch, max_len).total;
+    return plan_of(dims, heads, q_rows, batch, max_len, 0).total;
 }
 
 XP_API int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_t batch, int32_t max_pages,
@@ -755,7 +906,7 @@ XP_API int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows,
         !kv::aligned_to(workspace, 16))
         return XP_ERR_SHAPE;
     if (weights && (w_stride < (int64_t)max_pages * dims->page || !kv::aligned_to(weights, 4))) return XP_ERR_SHAPE;
-    const Launch p = plan_of(dims, heads, q_rows, batch, max_len);
+    const Launch p = plan_of(dims, heads, q_rows, batch, max_len, window);
     if (ws_bytes < p.total) return XP_ERR_WORKSPACE;
     char* ws = (char*)workspace;
     Args a{};
@@ -776,7 +927,9 @@ XP_API int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows,
     a.group = heads / dims->kv_heads;
     a.q_rows = q_rows;
     a.row_blocks = p.row_blocks;
-    a.splits = p.splits;
+    a.batch = batch;
+    a.share = p.share;
+    a.waves = p.waves;
     a.chunk = p.chunk;
     a.window = window;
     a.scale_m = (float)__builtin_frexp((double)scale * 1.4426950408889634, &a.scale_e);

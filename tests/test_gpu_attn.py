@@ -215,6 +215,25 @@ def test_decode_split_lengths(n, max_len, batch):
     check_decode(c, table, lens, q, out, 0.125, base=torch.zeros_like(w), weights=w)
 
 
+@pytest.mark.parametrize("batch,max_len", [(70, 12000), (64, 12000), (130, 100), (9, 12000)])
+def test_decode_ragged_batches(batch, max_len):
+    """One long sequence among many short and empty ones: cut and whole sequences in one launch,
+    in batches of more and of fewer sequences than lanes of a wave."""
+    rng = np.random.default_rng(batch)
+    kv, dim, page = 1, 64, 64
+    lens = rng.integers(0, 130, batch).astype(np.int32)
+    lens[batch // 2], lens[batch - 1], lens[0] = 11000, 3300, 0
+    cols = -(-11000 // page)
+    c = filled(rng, kv, dim, page, 250)
+    table = np.full((batch, cols), -1, dtype=np.int32)
+    for b in range(batch):                                 # sequences may share pages that are only read
+        n = -(-int(lens[b]) // page)
+        table[b, :n] = rng.permutation(250)[:n]
+    q = dev(rng.normal(size=(batch * 2, 3, dim)) * 2, torch.float16)
+    out = run_decode(c, on_device(c), table, lens, q, 0.125, q_rows=2, max_len=max_len)
+    check_decode(c, table, lens, q, out, 0.125, q_rows=2)
+
+
 def test_decode_lengths_out_of_range_are_clamped():
     rng = np.random.default_rng(8)
     c = filled(rng, 2, 64, 64, 6)
