@@ -49,115 +49,199 @@ struct RowMap {
     int rows;
 };
 
-// The row of this workgroup: its sequence's page-table row and position.
-// false: the row belongs to no sequence. pos is -1 where the cache has no such position.
-__device__ __forceinline__ bool place(const Geo& g, const RowMap& m, int row, const int32_t*& table_row, int& pos) {
-    const int b = sequence_of(m.cu, m.batch, row);
-    if (b >= m.batch) return false;
-    const long long p = (long long)m.start[b] + row - m.cu[b];
-    pos = p >= 0 && p < (long long)g.max_pages * g.page ? (int)p : -1;
-    table_row = m.table + (long long)b * g.max_pages;
-    return true;
+// Where a row's position lies: bytes of the cache to kv head 0's tile, -1 where the
+// cache has no such position, -2 for a row of no sequence; and its place in the tile.
+// b: the row's sequence or an earlier one.
+__device__ __forceinline__ long long place(const Geo& g, const RowMap& m, int row, int b, int& pos) {
+    pos = 0;
+    if (row >= m.rows) return -2;
+    while (b < m.batch && m.cu[b + 1] <= row) ++b;
+    if (b >= m.batch) return -2;
+    const long long at = (long long)m.start[b] + row - m.cu[b];
+    if (at < 0 || at >= (long long)g.max_pages * g.page) return -1;
+    pos = (int)at & 63;
+    return tile_at(g, m.table + (long long)b * g.max_pages, 0, (int)at);
+}
+// Bytes between kv heads' tiles of one page.
+__device__ __forceinline__ long long head_step(const Geo& g) { return (long long)(g.page / kTilePos) * tile_bytes(g.groups); }
+
+// A unit is 8 values of one row of k or v: per = 4 * groups units of k for each kv head,
+// as many of v. Where a unit lies in its tile:
+struct Unit {
+    int gi, part;   // group of 32 values, quarter of it
+    bool is_v;
+};
+__device__ __forceinline__ int code_at(const Geo& g, const Unit& u, int pos) {
+    return u.is_v ? v_code(g.groups, pos, 2 * u.gi + (u.part >> 1)) + 4 * (u.part & 1) : k_code(g.groups, pos, u.gi) + 4 * u.part;
+}
+__device__ __forceinline__ int scale_at(const Geo& g, const Unit& u, int pos) {
+    return u.is_v ? v_scale(g.groups, pos, u.gi) : k_scale(g.groups, pos, u.gi);
 }
 
-// Quantise: a row's 2 * kv_heads * head_dim values as units of 8, one a thread;
-// four neighbouring threads hold a group of 32 and share its scale (its largest
-// magnitude over two quad swaps). Bound by bytes: 2 (or 4) a value in, 4.25 bits
-// out. Each quad stores one chunk of 16 bytes of K or two of 8 of V; the lines
-// that neighbouring positions share meet in L2.
-template <int TYPE>
-__global__ __launch_bounds__(256) void append_kernel(Geo g, RowMap m, const void* __restrict__ k, long long ks,
-                                                     const void* __restrict__ v, long long vs, uint8_t* __restrict__ cache) {
-    const int row = blockIdx.x;
-    const int u = blockIdx.y * 256 + threadIdx.x;
-    const int per = g.kv_heads * g.groups * 4;       // units of one row of k
-    const int32_t* tr;
-    int pos;
-    if (!place(g, m, row, tr, pos) || pos < 0 || u >= 2 * per) return;   // per is a multiple of 8: quads stay whole
-    const bool is_v = u >= per;
-    const int w = is_v ? u - per : u;
-    float x[8];
-    load8<TYPE>(is_v ? v : k, (long long)row * (is_v ? vs : ks) + 8 * w, x);
-    float amax = 0.0f;
-    bool bad = false;                                 // fmax drops a NaN
+// One unit into its tile. Four neighbouring lanes hold a group and share its scale.
+__device__ __forceinline__ void quantise(const Geo& g, const Unit& u, const float x[8], uint8_t* tile, int pos) {
+    // magnitudes compare as integers, a NaN above infinity above every number
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        amax = fmaxf(amax, __builtin_fabsf(x[i]));
-        bad |= !(__builtin_fabsf(x[i]) < __builtin_inff());
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t a = __float_as_uint(x[j]) & 0x7fffffffu;
+        top = a > top ? a : top;
     }
-    amax = bad ? __builtin_inff() : amax;
-    amax = fmaxf(amax, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(amax), 0xB1, 0xF, 0xF, true)));
-    amax = fmaxf(amax, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(amax), 0x4E, 0xF, 0xF, true)));
-    const uint32_t sb = scale_byte(amax);
+    uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xF, 0xF, true);
+    top = o > top ? o : top;
+    o = (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E, 0xF, 0xF, true);
+    top = o > top ? o : top;
+    const uint32_t sb = scale_byte(__uint_as_float(top));
     const float s = e4m3_value(sb);
-    uint32_t codes = 0;
+    uint32_t codes;
+    if (sb == 0x7fu) {                               // not finite: signed zeros under a NaN scale
+        codes = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) codes |= e2m1_code(x[i], s) << (4 * i);
-    const int head = w / (g.groups * 4), gi = (w >> 2) % g.groups, part = w & 3;
-    const long long tile = tile_at(g, tr, head, pos);
-    if (tile < 0) return;
-    uint8_t* t = cache + tile;
-    const int p = pos & 63;
-    if (is_v) {
-        *(uint32_t*)(t + v_code(g.groups, p, 2 * gi + (part >> 1)) + 4 * (part & 1)) = codes;
-        if (part == 0) t[v_scale(g.groups, p, gi)] = (uint8_t)sb;
+        for (int j = 0; j < 8; ++j) codes |= __float_as_uint(x[j]) >> 31 << (4 * j + 3);
     } else {
-        *(uint32_t*)(t + k_code(g.groups, p, gi) + 4 * part) = codes;
-        if (part == 0) t[k_scale(g.groups, p, gi)] = (uint8_t)sb;
+        codes = e2m1_codes(x, s, s > 0.0f ? 1.0f / s : 0.0f);
     }
+    *(uint32_t*)(tile + code_at(g, u, pos)) = codes;
+    if (u.part == 0) tile[scale_at(g, u, pos)] = (uint8_t)sb;
 }
 
-// The reverse, exact in all three types: e2m1 times E4M3 has six significant
-// bits and lies within 2^-10 .. 2688. Positions the cache does not have read 0.
+// One unit out: e2m1 times E4M3 has six significant bits and lies within 2^-10 .. 2688,
+// so all three types hold it exactly.
 template <int TYPE>
-__global__ __launch_bounds__(256) void read_kernel(Geo g, RowMap m, const uint8_t* __restrict__ cache, void* __restrict__ k,
-                                                   long long ks, void* __restrict__ v, long long vs) {
+__device__ __forceinline__ void store8(void* out, long long at, uint32_t codes, float s) {
     typedef float f32x2v __attribute__((ext_vector_type(2)));
-    const int row = blockIdx.x;
-    const int u = blockIdx.y * 256 + threadIdx.x;
-    const int per = g.kv_heads * g.groups * 4;
-    const int32_t* tr;
-    int pos;
-    if (!place(g, m, row, tr, pos) || u >= 2 * per) return;
-    const bool is_v = u >= per;
-    const int w = is_v ? u - per : u;
-    const int head = w / (g.groups * 4), gi = (w >> 2) % g.groups, part = w & 3;
-    const long long tile = pos < 0 ? -1 : tile_at(g, tr, head, pos);
-    uint32_t codes = 0;
-    float s = 0.0f;
-    if (tile >= 0) {
-        const uint8_t* t = cache + tile;
-        const int p = pos & 63;
-        codes = *(const uint32_t*)(t + (is_v ? v_code(g.groups, p, 2 * gi + (part >> 1)) + 4 * (part & 1)
-                                             : k_code(g.groups, p, gi) + 4 * part));
-        s = e4m3_value(t[is_v ? v_scale(g.groups, p, gi) : k_scale(g.groups, p, gi)]);
-    }
-    f32x2v x[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1),
-                   __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3)};
-    void* out = is_v ? v : k;
-    const long long at = (long long)row * (is_v ? vs : ks) + 8 * w;
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[i].x *= s;
-        x[i].y *= s;
-        if constexpr (TYPE == XP_BF16)
-            o[i] = (uint32_t)bf16_rne(x[i].x) | (uint32_t)bf16_rne(x[i].y) << 16;
-        else if constexpr (TYPE == XP_F16)
-            o[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[i].x) |
-                   (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[i].y) << 16;
-    }
+    typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
+    const f32x2v x[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0) * s,
+                         __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1) * s,
+                         __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2) * s,
+                         __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3) * s};
     if constexpr (TYPE == XP_F32) {
         *(float4*)((float*)out + at) = float4{x[0].x, x[0].y, x[1].x, x[1].y};
         *(float4*)((float*)out + at + 4) = float4{x[2].x, x[2].y, x[3].x, x[3].y};
     } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            o[j] = TYPE == XP_BF16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(x[j], b16x2))
+                                   : __builtin_bit_cast(uint32_t, __builtin_convertvector(x[j], h16x2));
         *(uint4*)((uint16_t*)out + at) = uint4{o[0], o[1], o[2], o[3]};
     }
 }
 
+// Few rows: a workgroup takes 256 units of one row.
+template <int TYPE>
+__global__ __launch_bounds__(256) void append_row_kernel(Geo g, RowMap m, const void* __restrict__ k, long long ks,
+                                                         const void* __restrict__ v, long long vs, uint8_t* __restrict__ cache) {
+    const int row = blockIdx.x, n = blockIdx.y * 256 + threadIdx.x, per = g.kv_heads * g.groups * 4;
+    if (n >= 2 * per) return;                        // per is a multiple of 8: quads stay whole
+    const bool is_v = n >= per;
+    const int w = is_v ? n - per : n, head = w / (g.groups * 4);
+    float x[8];
+    load8<TYPE>(is_v ? v : k, (long long)row * (is_v ? vs : ks) + 8 * w, x);
+    int pos;
+    const long long tile = place(g, m, row, sequence_of(m.cu, m.batch, row), pos);
+    if (tile < 0) return;
+    quantise(g, Unit{(w >> 2) % g.groups, w & 3, is_v}, x, cache + tile + head * head_step(g), pos);
+}
+template <int TYPE>
+__global__ __launch_bounds__(256) void read_row_kernel(Geo g, RowMap m, const uint8_t* __restrict__ cache, void* __restrict__ k,
+                                                       long long ks, void* __restrict__ v, long long vs) {
+    const int row = blockIdx.x, n = blockIdx.y * 256 + threadIdx.x, per = g.kv_heads * g.groups * 4;
+    if (n >= 2 * per) return;
+    const bool is_v = n >= per;
+    const int w = is_v ? n - per : n, head = w / (g.groups * 4);
+    const Unit u{(w >> 2) % g.groups, w & 3, is_v};
+    int pos;
+    const long long tile = place(g, m, row, sequence_of(m.cu, m.batch, row), pos);
+    if (tile == -2) return;
+    const uint8_t* t = cache + (tile < 0 ? 0 : tile + head * head_step(g));
+    const uint32_t codes = tile < 0 ? 0u : *(const uint32_t*)(t + code_at(g, u, pos));
+    const float s = tile < 0 ? 0.0f : e4m3_value(t[scale_at(g, u, pos)]);
+    store8<TYPE>(is_v ? v : k, (long long)row * (is_v ? vs : ks) + 8 * w, codes, s);
+}
+
+// Many rows: a workgroup takes 64 rows of one kv head, so that the lines of a tile are
+// written and read by one workgroup (or two, where rows and tiles are not aligned) and
+// not by several chip parts with an L2 each. Bound by bytes: 2 (or 4) a value on one
+// side, 4.25 bits on the other.
+constexpr int kBlockRows = 64;
+constexpr int kBatchRows = 4;   // rows a thread has in flight
+struct Block {
+    int units, rows_each;       // units of a kv head (of k and v), rows the workgroup takes at once
+};
+__device__ __forceinline__ Block block_of(const Geo& g) { return Block{8 * g.groups, 256 / (8 * g.groups)}; }
+__device__ __forceinline__ void find_places(const Geo& g, const RowMap& m, int row0, long long* tile, int* pos) {
+    if (threadIdx.x < kBlockRows) {
+        int p;
+        tile[threadIdx.x] = place(g, m, row0 + threadIdx.x, sequence_of(m.cu, m.batch, row0), p);
+        pos[threadIdx.x] = p;
+    }
+    __syncthreads();
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void append_block_kernel(Geo g, RowMap m, const void* __restrict__ k, long long ks,
+                                                           const void* __restrict__ v, long long vs, uint8_t* __restrict__ cache) {
+    __shared__ long long tile[kBlockRows];
+    __shared__ int pos[kBlockRows];
+    const int row0 = (int)(blockIdx.x / g.kv_heads) * kBlockRows, head = blockIdx.x % g.kv_heads;
+    const Block bl = block_of(g);
+    const int n = threadIdx.x % bl.units, r0 = threadIdx.x / bl.units;
+    const Unit u{(n >> 2) % g.groups, n & 3, n >= 4 * g.groups};
+    const void* src = u.is_v ? v : k;
+    const long long stride = u.is_v ? vs : ks, col = (long long)head * g.groups * 32 + 8 * (n % (4 * g.groups));
+    const long long hs = head * head_step(g);
+    find_places(g, m, row0, tile, pos);
+    for (int r = r0; r < kBlockRows; r += kBatchRows * bl.rows_each) {
+        float x[kBatchRows][8];
+#pragma unroll
+        for (int i = 0; i < kBatchRows; ++i)         // 64 rows are whole batches for every head_dim
+            if (tile[r + i * bl.rows_each] >= 0) load8<TYPE>(src, (row0 + r + i * bl.rows_each) * stride + col, x[i]);
+#pragma unroll
+        for (int i = 0; i < kBatchRows; ++i) {
+            const long long t = tile[r + i * bl.rows_each];
+            if (t >= 0) quantise(g, u, x[i], cache + t + hs, pos[r + i * bl.rows_each]);
+        }
+    }
+}
+template <int TYPE>
+__global__ __launch_bounds__(256) void read_block_kernel(Geo g, RowMap m, const uint8_t* __restrict__ cache,
+                                                         void* __restrict__ k, long long ks, void* __restrict__ v, long long vs) {
+    __shared__ long long tile[kBlockRows];
+    __shared__ int pos[kBlockRows];
+    const int row0 = (int)(blockIdx.x / g.kv_heads) * kBlockRows, head = blockIdx.x % g.kv_heads;
+    const Block bl = block_of(g);
+    const int n = threadIdx.x % bl.units, r0 = threadIdx.x / bl.units;
+    const Unit u{(n >> 2) % g.groups, n & 3, n >= 4 * g.groups};
+    void* out = u.is_v ? v : k;
+    const long long stride = u.is_v ? vs : ks, col = (long long)head * g.groups * 32 + 8 * (n % (4 * g.groups));
+    const long long hs = head * head_step(g);
+    find_places(g, m, row0, tile, pos);
+    for (int r = r0; r < kBlockRows; r += kBatchRows * bl.rows_each) {
+        uint32_t codes[kBatchRows];
+        uint8_t sb[kBatchRows];
+#pragma unroll
+        for (int i = 0; i < kBatchRows; ++i) {
+            const long long t = tile[r + i * bl.rows_each];
+            const int p = pos[r + i * bl.rows_each];
+            codes[i] = t < 0 ? 0u : *(const uint32_t*)(cache + t + hs + code_at(g, u, p));
+            sb[i] = t < 0 ? (uint8_t)0 : cache[t + hs + scale_at(g, u, p)];
+        }
+#pragma unroll
+        for (int i = 0; i < kBatchRows; ++i)
+            if (tile[r + i * bl.rows_each] != -2)
+                store8<TYPE>(out, (row0 + r + i * bl.rows_each) * stride + col, codes[i], e4m3_value(sb[i]));
+    }
+}
+
+// Whether rows fill two workgroups of 64 on each of the 256 CUs.
+static bool many_rows(const Geo& g, int rows) { return (long long)rows / kBlockRows * g.kv_heads >= 512; }
+
 // ------------------------------------------------------------------ eviction
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
+constexpr int kSelKeys = 32768;     // positions whose keys are held in LDS; longer sequences read theirs again
 
 // Weights in the order of selection as unsigned keys: larger first, -0 as +0,
 // NaN below every number.
@@ -168,16 +252,18 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One workgroup per (sequence, kv head): the positions to keep, ascending. The
-// key of the last one kept among the unprotected positions is found by four
-// counting passes of eight bits (each wave counts into its own 256 bins); then
-// each wave walks its own run of positions, once to count and once to write.
+// One workgroup per (sequence, kv head): the positions to keep, ascending. The key of
+// the last one kept among the unprotected positions is found by three counting passes,
+// of 12, 10 and 10 bits: the first takes sign, exponent and three bits of the
+// significand, so weights that fall off over many powers of two spread over its bins.
+// Then each wave walks its own run of positions, once to count and once to write.
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(Geo g, const int32_t* __restrict__ lens,
                                                                    const float* weights, long long w_stride, int keep,
                                                                    int sinks, int recent, int32_t* kept,
                                                                    float* weights_out, long long wo_stride, int wo_len) {
-    __shared__ uint32_t bins[kSelWaves][256];
-    __shared__ uint32_t total[256];
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t bins[4096];
+    __shared__ int part[kSelWaves];
     __shared__ int pick[2];                       // the chosen bin and how many are wanted inside it
     __shared__ int n_over[kSelWaves], n_tie[kSelWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -195,55 +281,62 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(Geo g, const 
     } else {
         const int lo = sinks, hi = n - recent;
         int want = keep - sinks - recent;         // from [lo, hi), which holds more than that
-        uint32_t key = 0, known = 0;              // the leading bits of the last kept key
-        for (int shift = 24; want > 0 && shift >= 0; shift -= 8) {
-            for (int i = lane; i < 256; i += 64) bins[wave][i] = 0;
-            __syncthreads();
-            for (int i = lo + tid; i < hi; i += kSelThreads) {
-                const uint32_t k = weight_key(w[i]);
-                if ((k & known) == key) atomicAdd(&bins[wave][(k >> shift) & 255], 1u);
-            }
-            __syncthreads();
-            if (tid < 256) {
-                uint32_t s = 0;
-                for (int j = 0; j < kSelWaves; ++j) s += bins[j][tid];
-                total[tid] = s;
-            }
-            __syncthreads();
-            if (wave == 0) {
-                // lane holds bins 4*lane .. +3; `above`: counts of the bins over its own
-                const uint32_t t0 = total[4 * lane], t1 = total[4 * lane + 1], t2 = total[4 * lane + 2],
-                               t3 = total[4 * lane + 3];
-                const int own = (int)(t0 + t1 + t2 + t3);
-                const int upto = wave_incl_sum(own);
-                int above = __builtin_amdgcn_readlane(upto, 63) - upto;
-                const uint32_t t[4] = {t0, t1, t2, t3};
+        const bool any = want > 0, held_keys = n <= kSelKeys;
+        uint32_t key = 0;                         // of the last one kept
+        if (any) {
+            if (held_keys)
+                for (int i0 = lo; i0 < hi; i0 += 16 * kSelThreads) {
+                    float x[16];
 #pragma unroll
-                for (int j = 3; j >= 0; --j) {
-                    if (above < want && above + (int)t[j] >= want) {
-                        pick[0] = 4 * lane + j;
+                    for (int j = 0; j < 16; ++j) x[j] = i0 + j * kSelThreads + tid < hi ? w[i0 + j * kSelThreads + tid] : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (i0 + j * kSelThreads + tid < hi) keys[i0 + j * kSelThreads + tid] = weight_key(x[j]);
+                }
+            uint32_t known = 0;                   // its leading bits that are known
+#pragma unroll 1
+            for (int pass = 0; pass < 3; ++pass) {
+                const int shift = pass == 0 ? 20 : (pass == 1 ? 10 : 0), each = pass == 0 ? 4 : 1;
+                const uint32_t mask = pass == 0 ? 4095u : 1023u;
+                for (int i = tid; i < 4096; i += kSelThreads) bins[i] = 0;
+                __syncthreads();
+                for (int i = lo + tid; i < hi; i += kSelThreads) {
+                    const uint32_t k = held_keys ? keys[i] : weight_key(w[i]);
+                    if ((k & known) == key) atomicAdd(&bins[(k >> shift) & mask], 1u);
+                }
+                __syncthreads();
+                // a thread has `each` bins; `above`: counts of all the bins over its own
+                int own = 0;
+                for (int j = 0; j < each; ++j) own += (int)bins[tid * each + j];
+                const int upto = wave_incl_sum(own);
+                if (lane == 63) part[wave] = upto;
+                __syncthreads();
+                int above = part[wave] - upto;
+                for (int j = wave + 1; j < kSelWaves; ++j) above += part[j];
+                for (int j = each - 1; j >= 0; --j) {
+                    const int t = (int)bins[tid * each + j];
+                    if (above < want && above + t >= want) {
+                        pick[0] = tid * each + j;
                         pick[1] = want - above;
                     }
-                    above += (int)t[j];
+                    above += t;
                 }
+                __syncthreads();
+                key |= (uint32_t)pick[0] << shift;
+                known |= mask << shift;
+                want = pick[1];
             }
-            __syncthreads();
-            key |= (uint32_t)pick[0] << shift;
-            known |= 255u << shift;
-            want = pick[1];
-            __syncthreads();
         }
         // want: how many of the positions that hold exactly `key` are kept, the lowest first
-        const bool any = keep > sinks + recent;
         const int run = ((n + kSelThreads - 1) / kSelThreads) * 64;
         const int from = wave * run, to = from + run < n ? from + run : n;
         int over = 0, tie = 0;
         for (int i0 = from; i0 < to; i0 += 64) {
             const int i = i0 + lane;
-            const bool in = i < to, held = in && (i < lo || i >= hi);
-            const uint32_t k = in && !held ? weight_key(w[i]) : 0u;
-            over += __popcll(__ballot(held || (any && in && !held && k > key)));
-            tie += __popcll(__ballot(any && in && !held && k == key));
+            const bool in = i < to, held = in && (i < lo || i >= hi), free = any && in && !held;
+            const uint32_t k = free ? (held_keys ? keys[i] : weight_key(w[i])) : 0u;
+            over += __popcll(__ballot(held || (free && k > key)));
+            tie += __popcll(__ballot(free && k == key));
         }
         if (lane == 0) {
             n_over[wave] = over;
@@ -259,11 +352,11 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(Geo g, const 
         const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
         for (int i0 = from; i0 < to; i0 += 64) {
             const int i = i0 + lane;
-            const bool in = i < to, held = in && (i < lo || i >= hi);
-            const uint32_t k = in && !held ? weight_key(w[i]) : 0u;
-            const bool is_tie = any && in && !held && k == key;
+            const bool in = i < to, held = in && (i < lo || i >= hi), free = any && in && !held;
+            const uint32_t k = free ? (held_keys ? keys[i] : weight_key(w[i])) : 0u;
+            const bool is_tie = free && k == key;
             const uint64_t bt = __ballot(is_tie);
-            const bool yes = held || (any && in && !held && k > key) || (is_tie && ties + __popcll(bt & below) < want);
+            const bool yes = held || (free && k > key) || (is_tie && ties + __popcll(bt & below) < want);
             const uint64_t by = __ballot(yes);
             if (yes) out[at + __popcll(by & below)] = i;
             at += __popcll(by);
@@ -291,7 +384,7 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(Geo g, const 
     for (int i = m + tid; i < end; i += kSelThreads) wo[i] = 0.0f;
 }
 
-constexpr int kMoveThreads = 512;
+constexpr int kMoveThreads = 1024;
 constexpr int kMoveSteps = 4;
 
 // One workgroup per (group of 32 values of k or v, kv head, sequence): its kept
@@ -384,7 +477,8 @@ static int check_rows(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, 
                       const void* cache) {
     const int st = check_geo(dims, batch, max_pages);
     if (st != XP_OK) return st;
-    if (rows < 0 || type < XP_BF16 || type > XP_F32) return XP_ERR_SHAPE;
+    if (rows < 0 || rows > 0x7fffffff - 64 || (int64_t)rows * dims->kv_heads > 0xffffffffLL || type < XP_BF16 || type > XP_F32)
+        return XP_ERR_SHAPE;
     if (rows == 0 || batch == 0) return XP_OK;
     if (!k || !v || !cu || !start || !table || !cache) return XP_ERR_NULL;
     const int64_t width = (int64_t)dims->kv_heads * dims->head_dim, unit = type == XP_F32 ? 4 : 8;
@@ -395,6 +489,18 @@ static int check_rows(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, 
     return XP_OK;
 }
 
+#define XP_ROWS_LAUNCH(KERNEL_, TYPE_, ...)                                                                              \
+    do {                                                                                                                 \
+        if (many_rows(g, rows))                                                                                          \
+            hipLaunchKernelGGL(KERNEL_##_block_kernel<TYPE_>,                                                            \
+                               dim3((unsigned)g.kv_heads * (unsigned)((rows + kBlockRows - 1) / kBlockRows)), dim3(256), \
+                               0, s, __VA_ARGS__);                                                                       \
+        else                                                                                                             \
+            hipLaunchKernelGGL(KERNEL_##_row_kernel<TYPE_>,                                                              \
+                               dim3((unsigned)rows, (unsigned)((8 * g.kv_heads * g.groups + 255) / 256)), dim3(256), 0, s, \
+                               __VA_ARGS__);                                                                             \
+    } while (0)
+
 XP_API int xp_kv_append(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, int32_t type, const void* k,
                         int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_rows, const int32_t* start,
                         const int32_t* table, uint8_t* cache, void* stream) {
@@ -403,14 +509,16 @@ XP_API int xp_kv_append(const xp_kv_dims* dims, int32_t batch, int32_t max_pages
     if (rows == 0 || batch == 0) return XP_OK;
     const Geo g = geo_of(dims, max_pages);
     const RowMap m{cu_rows, start, table, batch, rows};
-    const dim3 grid((unsigned)rows, (unsigned)((2 * g.kv_heads * g.groups * 4 + 255) / 256));
     hipStream_t s = (hipStream_t)stream;
+#define XP_APPEND(TYPE_)                                                                                                 \
+    XP_ROWS_LAUNCH(append, TYPE_, g, m, k, (long long)k_stride, v, (long long)v_stride, cache)
     if (type == XP_BF16)
-        hipLaunchKernelGGL(append_kernel<XP_BF16>, grid, dim3(256), 0, s, g, m, k, k_stride, v, v_stride, cache);
+        XP_APPEND(XP_BF16);
     else if (type == XP_F16)
-        hipLaunchKernelGGL(append_kernel<XP_F16>, grid, dim3(256), 0, s, g, m, k, k_stride, v, v_stride, cache);
+        XP_APPEND(XP_F16);
     else
-        hipLaunchKernelGGL(append_kernel<XP_F32>, grid, dim3(256), 0, s, g, m, k, k_stride, v, v_stride, cache);
+        XP_APPEND(XP_F32);
+#undef XP_APPEND
     return launch_status();
 }
 
@@ -422,14 +530,15 @@ XP_API int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, 
     if (rows == 0 || batch == 0) return XP_OK;
     const Geo g = geo_of(dims, max_pages);
     const RowMap m{cu_rows, start, table, batch, rows};
-    const dim3 grid((unsigned)rows, (unsigned)((2 * g.kv_heads * g.groups * 4 + 255) / 256));
     hipStream_t s = (hipStream_t)stream;
+#define XP_READ(TYPE_) XP_ROWS_LAUNCH(read, TYPE_, g, m, cache, k, (long long)k_stride, v, (long long)v_stride)
     if (type == XP_BF16)
-        hipLaunchKernelGGL(read_kernel<XP_BF16>, grid, dim3(256), 0, s, g, m, cache, k, k_stride, v, v_stride);
+        XP_READ(XP_BF16);
     else if (type == XP_F16)
-        hipLaunchKernelGGL(read_kernel<XP_F16>, grid, dim3(256), 0, s, g, m, cache, k, k_stride, v, v_stride);
+        XP_READ(XP_F16);
     else
-        hipLaunchKernelGGL(read_kernel<XP_F32>, grid, dim3(256), 0, s, g, m, cache, k, k_stride, v, v_stride);
+        XP_READ(XP_F32);
+#undef XP_READ
     return launch_status();
 }
 
@@ -452,7 +561,9 @@ XP_API int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages,
     const Geo g = geo_of(dims, max_pages), d = geo_of(dims, dst_pages);
     hipStream_t s = (hipStream_t)stream;
     const int wo_len = wo_stride > 0x7fffffff ? 0x7fffffff : (int)wo_stride;
-    hipLaunchKernelGGL(evict_select_kernel, dim3(g.kv_heads, batch), dim3(kSelThreads), 0, s, g, lens, weights,
+    const int64_t most = (int64_t)max_pages * dims->page;
+    const unsigned held = (unsigned)(most < kSelKeys ? most : kSelKeys) * sizeof(uint32_t);
+    hipLaunchKernelGGL(evict_select_kernel, dim3(g.kv_heads, batch), dim3(kSelThreads), held, s, g, lens, weights,
                        (long long)w_stride, keep, sinks, recent, kept, weights_out, (long long)wo_stride, wo_len);
     const int rc = launch_status();
     if (rc != XP_OK) return rc;

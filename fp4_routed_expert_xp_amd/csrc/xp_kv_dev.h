@@ -67,14 +67,25 @@ __device__ __forceinline__ uint32_t scale_byte(float amax) {
     return (__float_as_uint(amax) & 0x7f800000u) == 0x7f800000u ? 0x7fu : (uint32_t)code;
 }
 
-// The e2m1 code nearest to v / s, ties to the even code, beyond 6 s to 6 s. The
-// seven midpoints times an E4M3 scale are exact in fp32, so no quotient is rounded.
-__device__ __forceinline__ uint32_t e2m1_code(float v, float s) {
-    const float a = __builtin_fabsf(v);
-    uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) +
-                 (a >= 3.5f * s) + (a > 5.0f * s);
-    c = s > 0.0f ? c : 0u;   // zero group, or a NaN scale
-    return c | (__float_as_uint(v) >> 31 << 3);
+// Eight e2m1 codes nearest to x / s, ties to the even code, beyond 6 s to 6 s; inv is
+// 1 / s. The quotient is corrected once by its exact remainder and so rounded to the
+// nearest fp32 number, which never crosses a midpoint of e2m1: a midpoint M times s is
+// an fp32 number, and x next to it lies 2^-23 / p away relative to it (p < 2 its
+// significand), more than half a step of M's, 2^-24 / m with M's significand m >= 1. A
+// quotient that is M itself comes out as M. The conversion rounds to nearest even.
+__device__ __forceinline__ uint32_t e2m1_codes(const float x[8], float s, float inv) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = x[i] * inv;
+        const float c = __builtin_fmaf(__builtin_fmaf(-q, s, x[i]), inv, q);
+        r[i] = __uint_as_float(__float_as_uint(c) | (__float_as_uint(x[i]) & 0x80000000u));   // -0 keeps its sign
+    }
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[0], r[1], 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[2], r[3], 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[4], r[5], 1.0f, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[6], r[7], 1.0f, 3);
 }
 
 inline bool geo_ok(const xp_kv_dims* d) {

@@ -448,6 +448,72 @@ def test_evict(kv, dim, page, keep, sinks, recent, in_place):
     np.testing.assert_array_equal(buf.cpu().numpy(), want.b.reshape(-1))
 
 
+@pytest.mark.parametrize("n,keep", [(20000, 5000), (32768, 30000), (40001, 123)])
+def test_evict_long(n, keep):
+    """Positions chosen from long contexts, below and beyond what the kernel holds on chip."""
+    rng = np.random.default_rng(n)
+    page = 256
+    cols = -(-n // page)
+    c = filled(rng, 2, 64, page, 4)
+    table = np.full((1, cols), -1, dtype=np.int32)         # the choice alone: nothing lies behind the table
+    dst = np.full((1, -(-keep // page)), -1, dtype=np.int32)
+    w = np.exp(rng.normal(size=(1, 2, cols * page)) * 8).astype(np.float32)
+    w[rng.random(w.shape) < 0.2] = 1e-3
+    w[0, 1] *= np.where(rng.random(cols * page) < 0.5, -1, 1).astype(np.float32)
+    buf = on_device(c)
+    kept, n_out, w_out = run_evict(c, buf, table, np.array([n], dtype=np.int32), w, keep, 4, 32, dst)
+    for h in range(2):
+        ids = ref.evict_list(w[0, h], n, keep, 4, 32)
+        np.testing.assert_array_equal(kept[0, h], ids)
+        np.testing.assert_array_equal(w_out[0, h, :keep], w[0, h, ids])
+    np.testing.assert_array_equal(buf.cpu().numpy(), c.b.reshape(-1))
+
+
+@pytest.mark.parametrize("kv,dim,ty", [(8, 64, "bf16"), (4, 128, "f32"), (2, 256, "f16")])
+def test_append_and_read_many_rows(kv, dim, ty):
+    """Enough rows for the form that takes 64 of them at a time, sequences beginning anywhere in a tile."""
+    rng = np.random.default_rng(dim)
+    counts = [9000, 0, 1, 70, 5000, 2300, 513]
+    if kv == 2:
+        counts[0] = 17000
+    start = [3, 0, 63, 64, 100, 17, 0]
+    cu, page = ends(counts), 192
+    cols = -(-(max(a + b for a, b in zip(counts, start))) // page)
+    used = [-(-(a + b) // page) for a, b in zip(counts, start)]
+    pages = sum(used) + 1
+    ids = rng.permutation(pages)
+    table = np.full((len(counts), cols), -1, dtype=np.int32)
+    at = 0
+    for b, u in enumerate(used):
+        table[b, :u] = ids[at:at + u]
+        at += u
+    table[0, 1] = -1                                       # a page that is missing
+    rows = int(cu[-1]) + 30
+    k, v = (torch.from_numpy(rng.normal(size=(rows, kv, dim)).astype(np.float32) * 3).to(DT[ty]) for _ in "kv")
+    d = xp.kv_dims(kv, dim, page, pages)
+    buf = torch.zeros(xp.xp_kv_bytes(d), dtype=torch.uint8, device="cuda")
+    xp.xp_kv_append(d, k.cuda(), v.cuda(), dev(cu), ints(start), dev(table), buf)
+    ko, vo = (torch.full((rows, kv, dim), 7.0, dtype=torch.float32, device="cuda") for _ in "kv")
+    xp.xp_kv_read(d, dev(cu), ints(start), dev(table), buf, ko, vo)
+    missing = np.zeros(rows, dtype=bool)
+    missing[page - 3:2 * page - 3] = True
+    missing = missing[:int(cu[-1])]
+    for x, o in ((k, ko), (v, vo)):
+        want = ref.values(*ref.quantise(x[:int(cu[-1])].double().numpy()))
+        want[missing] = 0.0
+        np.testing.assert_array_equal(o[:int(cu[-1])].double().cpu().numpy(), want)
+        assert (o[int(cu[-1]):] == 7.0).all()
+    # the bytes themselves: row by row through the small form, into a second cache
+    buf2 = torch.zeros_like(buf)
+    step = 400
+    for b in range(len(counts)):
+        for r in range(0, counts[b], step):
+            n = min(step, counts[b] - r)
+            s = slice(int(cu[b]) + r, int(cu[b]) + r + n)
+            xp.xp_kv_append(d, k[s].cuda(), v[s].cuda(), ints([0, n]), ints([start[b] + r]), dev(table[b:b + 1]), buf2)
+    assert torch.equal(buf, buf2)
+
+
 def test_evict_missing_pages():
     """A kept position without a page moves as zeros; a destination without one takes nothing."""
     rng = np.random.default_rng(6)
