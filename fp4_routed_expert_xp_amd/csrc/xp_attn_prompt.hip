@@ -23,6 +23,9 @@ typedef __attribute__((ext_vector_type(8))) short s16x8;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
+typedef __attribute__((address_space(3))) void* lptr;
+typedef __attribute__((address_space(1))) const void* gptr;
+
 constexpr int kRows = 128;   // rows of a workgroup: four waves of 32
 constexpr int kPos = 64;     // positions of a tile
 
@@ -170,8 +173,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
     constexpr int NS = D / 16;                 // contraction steps of the scores
     constexpr int ND = D / 32;                 // column blocks of the output
     constexpr int NL = kPos * D / 8 / 256;     // 16-byte chunks a thread stages of each of k and v
-    __shared__ __attribute__((aligned(16))) uint8_t lk[kPos * D * 2];
-    __shared__ __attribute__((aligned(16))) uint8_t lv[kPos * D * 2];
+    constexpr int kTile = kPos * D * 2;        // bytes of a tile of k, or of v
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * kTile];
 
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, hi = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -215,48 +218,54 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
 
     const uint16_t* kp = a.k + (long long)k0 * a.k_stride + (long long)head * D;
     const uint16_t* vp = a.v + (long long)k0 * a.v_stride + (long long)head * D;
-    uint4 ck[NL], cv[NL];
-    auto fetch = [&](int tile) {
+    // A tile goes straight from memory to LDS, one tile ahead into the other buffer: the
+    // j-th load of a thread fills LDS chunk j * 256 + tid, and reads the chunk that the
+    // permutation above puts there. Rows behind the last key repeat it (no row sees them).
+    const int lp = tid / (D / 8), lc = tid % (D / 8);
+    auto fetch = [&](int tile, uint8_t* to) {
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-            const int c = j * 256 + tid, pos = c / (D / 8), ch = c % (D / 8), p = tile * kPos + pos;
-            ck[j] = p < nk ? *(const uint4*)(kp + (long long)p * a.k_stride + 8 * ch) : uint4{0, 0, 0, 0};
-            cv[j] = p < nk ? *(const uint4*)(vp + (long long)p * a.v_stride + 8 * ch) : uint4{0, 0, 0, 0};
+            const int pos = j * (256 / (D / 8)) + lp;
+            int p = tile * kPos + pos;
+            p = p < nk ? p : nk - 1;
+            const int kc = (k_at<D>(pos, lc) - pos * (2 * D)) / 16, vc = (v_at<D>(pos, lc >> 2) - pos * (2 * D)) / 16 + (lc & 3);
+            uint8_t* d = to + j * 4096 + wave * 1024;
+            __builtin_amdgcn_global_load_lds((gptr)(kp + (long long)p * a.k_stride + 8 * kc), (lptr)d, 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((gptr)(vp + (long long)p * a.v_stride + 8 * vc), (lptr)(d + kTile), 16, 0, 0);
         }
     };
-    if (t_lo < t_hi) fetch(t_lo);
+    if (t_lo < t_hi) fetch(t_lo, lds[0]);
 
     for (int tile = t_lo; tile < t_hi; ++tile) {
         const bool masked = tile * kPos < full_lo || tile * kPos + kPos > full_hi;
-        __syncthreads();                       // the last tile is read
+        uint8_t* lk = lds[(tile - t_lo) & 1];
+        uint8_t* lv = lk + kTile;
+        // this wave's loads of the tile have landed, its reads of the last one are done; then everyone's
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (tile + 1 < t_hi) fetch(tile + 1, lds[(tile + 1 - t_lo) & 1]);
         bool bad = false;
+        if (masked) {
+            // a value of v that is not finite must not meet the zero weight of a row that does not see it
 #pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int c = j * 256 + tid, pos = c / (D / 8), ch = c % (D / 8);
-            *(uint4*)(lk + k_at<D>(pos, ch)) = ck[j];
-            *(uint4*)(lv + v_at<D>(pos, ch >> 2) + (ch & 3) * 16) = cv[j];
-            if (masked) {
-                const uint32_t u[4] = {cv[j].x, cv[j].y, cv[j].z, cv[j].w};
+            for (int j = 0; j < NL; ++j) {
+                const uint4 c = *(const uint4*)(lv + (j * 256 + tid) * 16);
+                const uint32_t u[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) bad |= not_finite<BF16>((uint16_t)u[i]) || not_finite<BF16>((uint16_t)(u[i] >> 16));
             }
-        }
-        // a value of v that is not finite must not meet the zero weight of a row that does not see it
-        if (masked)
             bad = __syncthreads_or(bad);
-        else
-            __syncthreads();
-        if (tile + 1 < t_hi) fetch(tile + 1);
+        }
 
         f32x16 s[2];
 #pragma unroll
-        for (int pb = 0; pb < 2; ++pb) {
+        for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[pb][r] = 0.0f;
 #pragma unroll
-            for (int st = 0; st < NS; ++st)
+        for (int st = 0; st < NS; ++st)
+#pragma unroll
+            for (int pb = 0; pb < 2; ++pb)
                 s[pb] = mma<BF16>(*(const s16x8*)(lk + k_at<D>(pb * 32 + m, 2 * st + hi)), qf[st], s[pb]);
-        }
         if (masked) {
 #pragma unroll
             for (int pb = 0; pb < 2; ++pb)
@@ -294,8 +303,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
             __syncthreads();                   // every wave has seen the tile as it was
 #pragma unroll
             for (int j = 0; j < NL; ++j) {
-                const int c = j * 256 + tid, pos = c / (D / 8), ch = c % (D / 8);
-                uint16_t* e = (uint16_t*)(lv + v_at<D>(pos, ch >> 2) + (ch & 3) * 16);
+                uint16_t* e = (uint16_t*)(lv + (j * 256 + tid) * 16);
                 for (int i = 0; i < 8; ++i)
                     if (not_finite<BF16>(e[i])) e[i] = 0;
             }
@@ -303,9 +311,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
         }
         const int i4 = (lane & 15) >> 2, col = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+        for (int st = 0; st < 4; ++st)
 #pragma unroll
-            for (int st = 0; st < 4; ++st) {
+            for (int d = 0; d < ND; ++d) {
                 const int pos = 16 * st + 4 * hi + i4;
                 o[d] = mma<BF16>(v_frag(lv + v_at<D>(pos, d) + col, lv + v_at<D>(pos + 8, d) + col), p[st], o[d]);
             }
