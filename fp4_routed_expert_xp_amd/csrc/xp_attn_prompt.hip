@@ -28,6 +28,7 @@ typedef __attribute__((address_space(1))) const void* gptr;
 
 constexpr int kRows = 128;   // rows of a workgroup: four waves of 32
 constexpr int kPos = 64;     // positions of a tile
+constexpr float kLag = 8.0f; // of the running maximum, in powers of two
 
 struct Args {
     const uint16_t* q;
@@ -222,16 +223,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
     // j-th load of a thread fills LDS chunk j * 256 + tid, and reads the chunk that the
     // permutation above puts there. Rows behind the last key repeat it (no row sees them).
     const int lp = tid / (D / 8), lc = tid % (D / 8);
+    constexpr int kStep = 256 / (D / 8);       // positions that one load of all threads covers
+    constexpr int kForms = D == 256 ? 2 : 1;   // permutations of a thread's loads: they repeat every 16 positions
+    uint32_t k_off[kForms], v_off[kForms];     // bytes from a load's first position
+#pragma unroll
+    for (int f = 0; f < kForms; ++f) {
+        const int pos = f * kStep + lp;
+        const int kc = (k_at<D>(pos, lc) - pos * (2 * D)) / 16, vc = (v_at<D>(pos, lc >> 2) - pos * (2 * D)) / 16 + (lc & 3);
+        k_off[f] = 2 * ((uint32_t)lp * (uint32_t)a.k_stride + 8 * kc);
+        v_off[f] = 2 * ((uint32_t)lp * (uint32_t)a.v_stride + 8 * vc);
+    }
     auto fetch = [&](int tile, uint8_t* to) {
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-            const int pos = j * (256 / (D / 8)) + lp;
-            int p = tile * kPos + pos;
-            p = p < nk ? p : nk - 1;
-            const int kc = (k_at<D>(pos, lc) - pos * (2 * D)) / 16, vc = (v_at<D>(pos, lc >> 2) - pos * (2 * D)) / 16 + (lc & 3);
+            const int p = tile * kPos + j * kStep, over = p + lp - (nk - 1);
+            const uint8_t* kj = (const uint8_t*)(kp + (long long)p * a.k_stride);
+            const uint8_t* vj = (const uint8_t*)(vp + (long long)p * a.v_stride);
             uint8_t* d = to + j * 4096 + wave * 1024;
-            __builtin_amdgcn_global_load_lds((gptr)(kp + (long long)p * a.k_stride + 8 * kc), (lptr)d, 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((gptr)(vp + (long long)p * a.v_stride + 8 * vc), (lptr)(d + kTile), 16, 0, 0);
+            if (tile * kPos + kPos <= nk) {
+                __builtin_amdgcn_global_load_lds((gptr)(kj + k_off[j % kForms]), (lptr)d, 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((gptr)(vj + v_off[j % kForms]), (lptr)(d + kTile), 16, 0, 0);
+            } else {
+                const long long back = over > 0 ? over : 0;
+                __builtin_amdgcn_global_load_lds((gptr)(kj + k_off[j % kForms] - 2 * back * a.k_stride), (lptr)d, 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((gptr)(vj + v_off[j % kForms] - 2 * back * a.v_stride), (lptr)(d + kTile), 16, 0, 0);
+            }
         }
     };
     if (t_lo < t_hi) fetch(t_lo, lds[0]);
@@ -279,7 +295,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
 #pragma unroll
         for (int r = 1; r < 32; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
         top = swap_max(top) * a.scale_log2;
-        if (__ballot(top > mx)) {
+        // Exponentials are taken from a maximum that lags behind by up to kLag: they stay below
+        // 2^kLag, and what was summed needs no factor but in a row's first tiles.
+        if (__ballot(top > mx + kLag)) {
             const float nm = fmaxf(top, mx);
             const float alpha = __builtin_amdgcn_exp2f(mx - (nm == -__builtin_inff() ? 0.0f : nm));
             mx = nm;
@@ -357,6 +375,8 @@ XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int
     if (batch == 0 || rows_q == 0) return XP_OK;
     if (!q || !cu_q || !cu_k || !out || (rows_k > 0 && (!k || !v))) return XP_ERR_NULL;
     const int64_t qw = (int64_t)heads * head_dim, kw = (int64_t)kv_heads * head_dim;
+    const int64_t far = (int64_t)1 << 24;   // a load's offsets within 32 rows of k and v are 32-bit
+    if (k_stride >= far || v_stride >= far) return XP_ERR_SHAPE;
     if (q_stride < qw || out_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
         out_stride % 4 || !kv::aligned_to(q, 16) || !kv::aligned_to(k, 16) || !kv::aligned_to(v, 16) || !kv::aligned_to(out, 8) || !kv::aligned_to(cu_q, 4) || !kv::aligned_to(cu_k, 4))
         return XP_ERR_SHAPE;

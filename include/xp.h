@@ -440,7 +440,8 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
  * cu_q[b] .. cu_q[b+1] - 1 of q and out and cu_k[b] .. cu_k[b+1] - 1 of k and v.
  * Its last query sits at its last key's position, so a prompt's later piece may
  * attend to the earlier pieces' keys; a query before its first key sees nothing.
- * Rows of out from cu_q[batch] on are left as they were. */
+ * Rows of out from cu_q[batch] on are left as they were. Strides of k and v are below
+ * 2^24 elements. */
 int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch, int32_t rows_q, int32_t rows_k,
                    int32_t type, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                    int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, float scale, int32_t window, void* out,

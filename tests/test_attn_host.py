@@ -132,7 +132,7 @@ def test_prompt_refuses():
     for kw in (dict(heads=0), dict(kv=0), dict(heads=3), dict(kv=1025, heads=1025), dict(dim=32), dict(dim=96), dict(dim=0),
                dict(batch=-1), dict(batch=65536), dict(rq=-1), dict(rk=-1), dict(ty=F32), dict(ty=-1), dict(window=-1),
                dict(scale=0.0), dict(scale=-2.0), dict(scale=inf), dict(scale=nan), dict(qs=248), dict(ks=120), dict(vs=120),
-               dict(os=248), dict(qs=258), dict(ks=132), dict(vs=130), dict(os=258), dict(q=ODD), dict(k=ODD), dict(v=ODD),
+               dict(os=248), dict(ks=1 << 24), dict(vs=1 << 24), dict(qs=258), dict(ks=132), dict(vs=130), dict(os=258), dict(q=ODD), dict(k=ODD), dict(v=ODD),
                dict(out=ODD), dict(cq=ctypes.c_void_p(0x1002)), dict(rq=0x7fffffff), dict(rk=0x7fffffff)):
         assert call(**kw) == xp.XP_ERR_SHAPE, kw
     assert call(rq=0, q=None, out=None) == xp.XP_OK
