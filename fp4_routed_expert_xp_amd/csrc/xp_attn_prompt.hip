@@ -3,12 +3,20 @@
 //
 // One pass over the keys with a running maximum and sum. A row is a (token, head of
 // the kv head's group) pair, tokens first, so the heads that share keys share a
-// workgroup and a short prompt still fills its 128 rows. A wave owns 32 rows and
-// takes 64 positions at a time: S^T = K Q^T (v_mfma_f32_32x32x16, positions as the
-// matrix rows) leaves lane (m, hi) = (lane % 32, lane / 32) with row m at positions
-// 8 a + 4 hi + i of each 32, so the exponentials, once rounded, are the operand of
-// O^T += V^T P^T where they are: V follows the same order of positions through the
-// 16-bit transposing LDS read, which hands a lane four positions of one column.
+// workgroup and a short prompt still fills its 128 rows. A wave owns RW rows and takes
+// 64 positions at a time. S^T = K Q^T (v_mfma_f32_32x32x16 for 32 rows, 16x16x32 for
+// 16; positions as the matrix rows) leaves lane (m, q) = (lane % RW, lane / RW) with
+// row m at every fourth quad of positions, so the exponentials, once rounded, are the
+// operand of O^T += V^T P^T where they are: V follows the same order of positions
+// through the 16-bit transposing LDS read, which hands a lane four positions of one
+// column.
+//
+// Waves of 32 rows read k and v from LDS half as often; their registers (outputs,
+// scores, q) leave two waves a SIMD up to 128 columns and one at 256, where waves of 16
+// rows leave two: 8 heads of 256 over 4,096 rows take 157 us in those and 233 us in
+// waves of 32, 32 heads of 128 over 8,192 rows 635 us in waves of 16 and 581 us in 32.
+// Bound there by the matrix pipes (44% busy) and the vector pipes (46%, the
+// exponentials most of it), which overlap for a sixth of the time.
 //
 // Scores, maxima, sums and outputs are fp32; exponentials round once to the type of
 // v (the product's operand), the result once to the output type.
@@ -21,12 +29,11 @@ typedef __attribute__((ext_vector_type(8))) _Float16 h16x8;
 typedef __attribute__((ext_vector_type(8))) __bf16 b16x8;
 typedef __attribute__((ext_vector_type(8))) short s16x8;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
-typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 typedef __attribute__((address_space(3))) void* lptr;
 typedef __attribute__((address_space(1))) const void* gptr;
 
-constexpr int kRows = 128;   // rows of a workgroup: four waves of 32
+constexpr int kRows = 128;   // rows of a workgroup
 constexpr int kPos = 64;     // positions of a tile
 constexpr float kLag = 8.0f; // of the running maximum, in powers of two
 
@@ -42,12 +49,24 @@ struct Args {
     float scale_log2;
 };
 
-template <bool BF16>
-__device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
-    if constexpr (BF16)
+// What a wave of RW rows has of its products: RW x RW results, VE a lane, over KD of
+// the contraction; lane (m, q) holds column m and, as element r, row at(r, q).
+template <int RW>
+struct Shape {
+    static constexpr int VE = RW * RW / 64, KD = 512 / RW, NQ = 64 / RW;
+    typedef __attribute__((ext_vector_type(VE))) float acc;
+    static __device__ __forceinline__ int at(int r, int q) { return 4 * NQ * (r >> 2) + 4 * q + (r & 3); }
+};
+template <int RW, bool BF16>
+__device__ __forceinline__ typename Shape<RW>::acc mma(s16x8 a, s16x8 b, typename Shape<RW>::acc c) {
+    if constexpr (RW == 32 && BF16)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
-    else
+    else if constexpr (RW == 32)
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h16x8, a), __builtin_bit_cast(h16x8, b), c, 0, 0, 0);
+    else if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h16x8, a), __builtin_bit_cast(h16x8, b), c, 0, 0, 0);
 }
 
 // 16 bits of the operand type, nearest even.
@@ -63,29 +82,39 @@ __device__ __forceinline__ bool not_finite(uint16_t u) {
     return (u & e) == e;
 }
 
-__device__ __forceinline__ float swap_max(float x) {
+// Largest (or sum) over the lanes that share a row.
+template <int RW, bool SUM>
+__device__ __forceinline__ float over_q(float x) {
+    const auto join = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
     const uint32_t u = __float_as_uint(x);
     const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-}
-__device__ __forceinline__ float swap_sum(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    x = join(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    if constexpr (RW == 16) {
+        const uint32_t w = __float_as_uint(x);
+        const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+        x = join(__uint_as_float(b[0]), __uint_as_float(b[1]));
+    }
+    return x;
 }
 
 // LDS places. K: a row's 16-byte chunks are permuted so that 16 neighbouring rows at
-// one chunk index cover all banks; V: its 64-byte blocks, so that the eight rows of a
-// transposing read meet each bank twice at most.
+// one chunk index cover all banks; V: its blocks of RW columns, so that the rows of a
+// transposing read (eight of 64 bytes, or sixteen of 32) meet each bank twice at most.
 template <int D>
 __device__ __forceinline__ int k_at(int pos, int chunk) {
     const int s = D == 64 ? (pos >> 1) & 7 : pos & 15;
     return pos * (2 * D) + (chunk ^ s) * 16;
 }
-template <int D>
+template <int D, int RW>
 __device__ __forceinline__ int v_at(int pos, int block) {
-    const int s = D == 64 ? (pos >> 1) & 1 : pos & 3;
-    return pos * (2 * D) + (block ^ s) * 64;
+    const int s = RW == 32 ? (D == 64 ? (pos >> 1) & 1 : pos & 3) : (D == 64 ? (pos >> 1) & 3 : pos & 7);
+    return pos * (2 * D) + (block ^ s) * (2 * RW);
+}
+// Chunk of 16 bytes of a row of v that LDS chunk c of the row holds.
+template <int D, int RW>
+__device__ __forceinline__ int v_chunk(int pos, int c) {
+    constexpr int per = RW / 8;                // chunks of a block
+    return (v_at<D, RW>(pos, c / per) - pos * (2 * D)) / 16 + c % per;
 }
 
 __device__ __forceinline__ s16x8 v_frag(const uint8_t* a, const uint8_t* b) {
@@ -98,23 +127,24 @@ __device__ __forceinline__ s16x8 v_frag(const uint8_t* a, const uint8_t* b) {
 // finite: a zero weight times one of those is NaN, so they are taken out of the tile
 // and added here, to the rows that see them. One product per kind (+inf, -inf, NaN)
 // of its places with what each row sees counts the seen ones of each column.
-template <int D, bool BF16>
-__device__ __forceinline__ void set_apart(f32x16 (&o)[D / 32], const uint8_t* lv, int first, int at, int lo) {
+template <int D, int RW, bool BF16>
+__device__ __forceinline__ void set_apart(typename Shape<RW>::acc (&o)[D / RW], const uint8_t* lv, int first, int at, int lo) {
     constexpr short one = BF16 ? 0x3f80 : 0x3c00;
     constexpr uint16_t inf = BF16 ? 0x7f80 : 0x7c00;
-    const int lane = threadIdx.x & 63, hi = lane >> 5;
-    const int i4 = (lane & 15) >> 2, col = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    constexpr int KD = Shape<RW>::KD, VE = Shape<RW>::VE;
+    const int lane = threadIdx.x & 63, q = lane / RW;
+    const int row = 4 * q + ((lane & 15) >> 2), col = ((lane % RW) >> 4) * 32 + (lane & 3) * 8;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+    for (int d = 0; d < D / RW; ++d)
 #pragma unroll 1
         for (int kind = 0; kind < 3; ++kind) {
-            f32x16 n;
+            typename Shape<RW>::acc n;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) n[r] = 0.0f;
+            for (int r = 0; r < VE; ++r) n[r] = 0.0f;
 #pragma unroll 1
-            for (int st = 0; st < 4; ++st) {
-                const int pos = 16 * st + 4 * hi + i4;
-                const s16x8 vf = v_frag(lv + v_at<D>(pos, d) + col, lv + v_at<D>(pos + 8, d) + col);
+            for (int st = 0; st < kPos / KD; ++st) {
+                const int pos = KD * st + row;
+                const s16x8 vf = v_frag(lv + v_at<D, RW>(pos, d) + col, lv + v_at<D, RW>(pos + KD / 2, d) + col);
                 s16x8 f, seen;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -122,14 +152,14 @@ __device__ __forceinline__ void set_apart(f32x16 (&o)[D / 32], const uint8_t* lv
                     const bool is = kind == 0 ? u == inf : (kind == 1 ? u == (inf | 0x8000)
                                                                       : not_finite<BF16>(u) && (u & 0x7fff) != inf);
                     f[j] = is ? one : (short)0;
-                    const int ps = first + 16 * st + 8 * (j >> 2) + 4 * hi + (j & 3);
+                    const int ps = first + KD * st + KD / 2 * (j >> 2) + 4 * q + (j & 3);
                     seen[j] = ps <= at && ps >= lo ? one : (short)0;
                 }
-                n = mma<BF16>(f, seen, n);
+                n = mma<RW, BF16>(f, seen, n);
             }
             const float add = kind == 0 ? __builtin_inff() : (kind == 1 ? -__builtin_inff() : __builtin_nanf(""));
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
+            for (int r = 0; r < VE; ++r)
                 if (n[r] > 0.0f) o[d][r] += add;
         }
 }
@@ -169,15 +199,19 @@ __device__ __forceinline__ bool find_block(const Args& a, int blk, int& seq, int
     return false;
 }
 
-template <int D, bool BF16>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args a) {
-    constexpr int NS = D / 16;                 // contraction steps of the scores
-    constexpr int ND = D / 32;                 // column blocks of the output
-    constexpr int NL = kPos * D / 8 / 256;     // 16-byte chunks a thread stages of each of k and v
+template <int D, int RW, bool BF16>
+__global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a) {
+    typedef Shape<RW> Sh;
+    typedef typename Sh::acc acc;
+    constexpr int KD = Sh::KD, VE = Sh::VE, kThreads = 64 * kRows / RW;
+    constexpr int NS = D / KD;                 // contraction steps of the scores
+    constexpr int NT = kPos / RW;              // blocks of positions of the scores
+    constexpr int ND = D / RW;                 // column blocks of the output
+    constexpr int NL = kPos * D / 8 / kThreads;   // 16-byte chunks a thread stages of each of k and v
     constexpr int kTile = kPos * D * 2;        // bytes of a tile of k, or of v
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * kTile];
 
-    const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, hi = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, m = lane % RW, q = lane / RW;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int head = blockIdx.x % a.kv_heads;
     int b, first;
@@ -190,7 +224,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
     const int nk = k1 - k0, shift = nk - nq;   // token i sits at position i + shift
 
     const int rows = nq * a.group;
-    const int row = first + wave * 32 + m;
+    const int row = first + wave * RW + m;
     const bool live = row < rows;
     const int tok = live ? row / a.group : 0;
     const int hd = head * a.group + (live ? row - tok * a.group : 0);
@@ -198,9 +232,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
     const int lo = a.window > 0 && at - a.window + 1 > 0 ? at - a.window + 1 : 0;
 
     s16x8 qf[NS];
-    const uint16_t* qp = a.q + (long long)(q0 + tok) * a.q_stride + (long long)hd * D + 8 * hi;
+    const uint16_t* qp = a.q + (long long)(q0 + tok) * a.q_stride + (long long)hd * D + 8 * q;
 #pragma unroll
-    for (int st = 0; st < NS; ++st) qf[st] = live ? *(const s16x8*)(qp + 16 * st) : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+    for (int st = 0; st < NS; ++st) qf[st] = live ? *(const s16x8*)(qp + KD * st) : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
 
     // tiles that some row of the workgroup sees, and those that all see whole
     const int last_row = first + kRows < rows ? first + kRows - 1 : rows - 1;
@@ -210,43 +244,38 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
     const int t_lo = a.window > 0 && w_first > 0 ? w_first >> 6 : 0;
     const int full_lo = a.window > 0 && w_last > 0 ? w_last : 0, full_hi = at_first + 1;
 
-    f32x16 o[ND];
+    acc o[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+        for (int r = 0; r < VE; ++r) o[d][r] = 0.0f;
     float mx = -__builtin_inff(), sum = 0.0f;
 
     const uint16_t* kp = a.k + (long long)k0 * a.k_stride + (long long)head * D;
     const uint16_t* vp = a.v + (long long)k0 * a.v_stride + (long long)head * D;
     // A tile goes straight from memory to LDS, one tile ahead into the other buffer: the
-    // j-th load of a thread fills LDS chunk j * 256 + tid, and reads the chunk that the
+    // j-th load of a thread fills LDS chunk j * kThreads + tid, and reads the chunk that the
     // permutation above puts there. Rows behind the last key repeat it (no row sees them).
     const int lp = tid / (D / 8), lc = tid % (D / 8);
-    constexpr int kStep = 256 / (D / 8);       // positions that one load of all threads covers
-    constexpr int kForms = D == 256 ? 2 : 1;   // permutations of a thread's loads: they repeat every 16 positions
-    uint32_t k_off[kForms], v_off[kForms];     // bytes from a load's first position
-#pragma unroll
-    for (int f = 0; f < kForms; ++f) {
-        const int pos = f * kStep + lp;
-        const int kc = (k_at<D>(pos, lc) - pos * (2 * D)) / 16, vc = (v_at<D>(pos, lc >> 2) - pos * (2 * D)) / 16 + (lc & 3);
-        k_off[f] = 2 * ((uint32_t)lp * (uint32_t)a.k_stride + 8 * kc);
-        v_off[f] = 2 * ((uint32_t)lp * (uint32_t)a.v_stride + 8 * vc);
-    }
+    constexpr int kStep = kThreads / (D / 8);  // positions that one load of all threads covers: whole
+    static_assert(kStep % 16 == 0);            // sixteens, which the permutations repeat after
+    const int kc = (k_at<D>(lp, lc) - lp * (2 * D)) / 16, vc = v_chunk<D, RW>(lp, lc);
+    const uint32_t k_off = 2 * ((uint32_t)lp * (uint32_t)a.k_stride + 8 * kc);   // bytes from a load's first position
+    const uint32_t v_off = 2 * ((uint32_t)lp * (uint32_t)a.v_stride + 8 * vc);
     auto fetch = [&](int tile, uint8_t* to) {
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
             const int p = tile * kPos + j * kStep, over = p + lp - (nk - 1);
             const uint8_t* kj = (const uint8_t*)(kp + (long long)p * a.k_stride);
             const uint8_t* vj = (const uint8_t*)(vp + (long long)p * a.v_stride);
-            uint8_t* d = to + j * 4096 + wave * 1024;
+            uint8_t* d = to + j * (16 * kThreads) + wave * 1024;
             if (tile * kPos + kPos <= nk) {
-                __builtin_amdgcn_global_load_lds((gptr)(kj + k_off[j % kForms]), (lptr)d, 16, 0, 0);
-                __builtin_amdgcn_global_load_lds((gptr)(vj + v_off[j % kForms]), (lptr)(d + kTile), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((gptr)(kj + k_off), (lptr)d, 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((gptr)(vj + v_off), (lptr)(d + kTile), 16, 0, 0);
             } else {
                 const long long back = over > 0 ? over : 0;
-                __builtin_amdgcn_global_load_lds((gptr)(kj + k_off[j % kForms] - 2 * back * a.k_stride), (lptr)d, 16, 0, 0);
-                __builtin_amdgcn_global_load_lds((gptr)(vj + v_off[j % kForms] - 2 * back * a.v_stride), (lptr)(d + kTile), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((gptr)(kj + k_off - 2 * back * a.k_stride), (lptr)d, 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((gptr)(vj + v_off - 2 * back * a.v_stride), (lptr)(d + kTile), 16, 0, 0);
             }
         }
     };
@@ -264,7 +293,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
             // a value of v that is not finite must not meet the zero weight of a row that does not see it
 #pragma unroll
             for (int j = 0; j < NL; ++j) {
-                const uint4 c = *(const uint4*)(lv + (j * 256 + tid) * 16);
+                const uint4 c = *(const uint4*)(lv + (j * kThreads + tid) * 16);
                 const uint32_t u[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) bad |= not_finite<BF16>((uint16_t)u[i]) || not_finite<BF16>((uint16_t)(u[i] >> 16));
@@ -272,29 +301,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
             bad = __syncthreads_or(bad);
         }
 
-        f32x16 s[2];
+        acc s[NT];
 #pragma unroll
-        for (int pb = 0; pb < 2; ++pb)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[pb][r] = 0.0f;
+            for (int r = 0; r < VE; ++r) s[t][r] = 0.0f;
 #pragma unroll
         for (int st = 0; st < NS; ++st)
 #pragma unroll
-            for (int pb = 0; pb < 2; ++pb)
-                s[pb] = mma<BF16>(*(const s16x8*)(lk + k_at<D>(pb * 32 + m, 2 * st + hi)), qf[st], s[pb]);
+            for (int t = 0; t < NT; ++t)
+                s[t] = mma<RW, BF16>(*(const s16x8*)(lk + k_at<D>(RW * t + m, KD / 8 * st + q)), qf[st], s[t]);
         if (masked) {
 #pragma unroll
-            for (int pb = 0; pb < 2; ++pb)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int p = tile * kPos + pb * 32 + 8 * (r >> 2) + 4 * hi + (r & 3);
-                    if (p > at || p < lo) s[pb][r] = -__builtin_inff();
-                }
+            for (int e = 0; e < NT * VE; ++e) {
+                const int p = tile * kPos + RW * (e / VE) + Sh::at(e % VE, q);
+                if (p > at || p < lo) s[e / VE][e % VE] = -__builtin_inff();
+            }
         }
         float top = s[0][0];
 #pragma unroll
-        for (int r = 1; r < 32; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
-        top = swap_max(top) * a.scale_log2;
+        for (int e = 1; e < NT * VE; ++e) top = fmaxf(top, s[e / VE][e % VE]);
+        top = over_q<RW, false>(top) * a.scale_log2;
         // Exponentials are taken from a maximum that lags behind by up to kLag: they stay below
         // 2^kLag, and what was summed needs no factor but in a row's first tiles.
         if (__ballot(top > mx + kLag)) {
@@ -306,51 +333,51 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt_kernel(Args
             for (int d = 0; d < ND; ++d) o[d] *= alpha;
         }
         const float base = mx == -__builtin_inff() ? 0.0f : -mx;
-        s16x8 p[4];
+        s16x8 p[NT * VE / 8];
         float add = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) {
-            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r >> 4][r & 15], a.scale_log2, base));
+        for (int e = 0; e < NT * VE; ++e) {
+            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e / VE][e % VE], a.scale_log2, base));
             add += x;
-            p[r >> 3][r & 7] = half_of<BF16>(x);
+            p[e >> 3][e & 7] = half_of<BF16>(x);
         }
         sum += add;
 
         if (masked && bad) {
-            set_apart<D, BF16>(o, lv, tile * kPos, at, lo);
+            set_apart<D, RW, BF16>(o, lv, tile * kPos, at, lo);
             __syncthreads();                   // every wave has seen the tile as it was
 #pragma unroll
             for (int j = 0; j < NL; ++j) {
-                uint16_t* e = (uint16_t*)(lv + (j * 256 + tid) * 16);
+                uint16_t* e = (uint16_t*)(lv + (j * kThreads + tid) * 16);
                 for (int i = 0; i < 8; ++i)
                     if (not_finite<BF16>(e[i])) e[i] = 0;
             }
             __syncthreads();
         }
-        const int i4 = (lane & 15) >> 2, col = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+        const int vrow = 4 * q + ((lane & 15) >> 2), col = (m >> 4) * 32 + (lane & 3) * 8;
 #pragma unroll
-        for (int st = 0; st < 4; ++st)
+        for (int st = 0; st < kPos / KD; ++st)
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const int pos = 16 * st + 4 * hi + i4;
-                o[d] = mma<BF16>(v_frag(lv + v_at<D>(pos, d) + col, lv + v_at<D>(pos + 8, d) + col), p[st], o[d]);
+                const int pos = KD * st + vrow;
+                o[d] = mma<RW, BF16>(v_frag(lv + v_at<D, RW>(pos, d) + col, lv + v_at<D, RW>(pos + KD / 2, d) + col), p[st], o[d]);
             }
     }
 
-    sum = swap_sum(sum);
+    sum = over_q<RW, true>(sum);
     if (!live) return;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;      // nothing seen: zeros
-    uint16_t* y = a.out + (long long)(q0 + tok) * a.out_stride + (long long)hd * D + 4 * hi;
+    uint16_t* y = a.out + (long long)(q0 + tok) * a.out_stride + (long long)hd * D;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < VE; e += 4) {
             uint32_t w[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                w[j] = (uint32_t)(uint16_t)half_of<BF16>(o[d][4 * e + 2 * j] * inv) |
-                       (uint32_t)(uint16_t)half_of<BF16>(o[d][4 * e + 2 * j + 1] * inv) << 16;
-            *(uint2*)(y + 32 * d + 8 * e) = uint2{w[0], w[1]};
+                w[j] = (uint32_t)(uint16_t)half_of<BF16>(o[d][e + 2 * j] * inv) |
+                       (uint32_t)(uint16_t)half_of<BF16>(o[d][e + 2 * j + 1] * inv) << 16;
+            *(uint2*)(y + RW * d + Sh::at(e, q)) = uint2{w[0], w[1]};
         }
 }
 
@@ -382,21 +409,22 @@ XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int
         return XP_ERR_SHAPE;
     const Args a{(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)out, q_stride, k_stride, v_stride,
                  out_stride, cu_q, cu_k, rows_q, rows_k, batch, kv_heads, group, window, kv::log2_scale(scale)};
-    const dim3 grid((unsigned)(blocks * kv_heads)), block(256);
+    const dim3 grid((unsigned)(blocks * kv_heads));
     hipStream_t s = (hipStream_t)stream;
-#define XP_PROMPT_LAUNCH(D_)                                                                       \
+#define XP_PROMPT_LAUNCH(D_, RW_)                                                                  \
     do {                                                                                           \
+        const dim3 block(64 * kRows / RW_);                                                        \
         if (type == XP_BF16)                                                                       \
-            hipLaunchKernelGGL((attn_prompt_kernel<D_, true>), grid, block, 0, s, a);              \
+            hipLaunchKernelGGL((attn_prompt_kernel<D_, RW_, true>), grid, block, 0, s, a);         \
         else                                                                                       \
-            hipLaunchKernelGGL((attn_prompt_kernel<D_, false>), grid, block, 0, s, a);             \
+            hipLaunchKernelGGL((attn_prompt_kernel<D_, RW_, false>), grid, block, 0, s, a);        \
     } while (0)
     if (head_dim == 64)
-        XP_PROMPT_LAUNCH(64);
+        XP_PROMPT_LAUNCH(64, 32);
     else if (head_dim == 128)
-        XP_PROMPT_LAUNCH(128);
+        XP_PROMPT_LAUNCH(128, 32);
     else
-        XP_PROMPT_LAUNCH(256);
+        XP_PROMPT_LAUNCH(256, 16);
 #undef XP_PROMPT_LAUNCH
     return launch_status();
 }
