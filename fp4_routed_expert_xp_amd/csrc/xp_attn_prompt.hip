@@ -164,20 +164,42 @@ __device__ __forceinline__ void set_apart(typename Shape<RW>::acc (&o)[D / RW], 
         }
 }
 
-// The workgroup's block of rows: sequence and first row, the longest-running (last)
-// blocks of the packed batch first. false: no such block.
+__device__ __forceinline__ int blocks_of(const Args& a, int b) {
+    if (b >= a.batch) return 0;
+    const long long rows = (long long)a.cu_q[b + 1] - a.cu_q[b];
+    return rows > 0 && rows <= a.rows_q ? (int)((rows * a.group + kRows - 1) / kRows) : 0;
+}
+// The workgroup's block of rows: sequence and first row. The blocks that run longest,
+// the last ones of their sequences, come first, so that short ones fill the gaps at the
+// end: among up to 64 sequences by their number in the sequence, else each sequence's
+// from its last to its first. false: no such block.
 __device__ __forceinline__ bool find_block(const Args& a, int blk, int& seq, int& first) {
     const int lane = threadIdx.x & 63;
+    if (a.batch <= 64) {
+        const int n = blocks_of(a, lane);
+        // blocks numbered k or more: the sum of max(0, n - k); find the k of block blk
+        const auto from = [&](int k) { return __builtin_amdgcn_readlane(wave_incl_sum(n > k ? n - k : 0), 63); };
+        if (blk >= from(0)) return false;
+        int lo = 0, hi = (int)wave_max_u32((uint32_t)n);       // from(lo) > blk >= from(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (from(mid) > blk)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const uint64_t there = __ballot(n > lo);
+        const int at = blk - from(lo + 1);
+        const uint64_t hit = __ballot(n > lo && __popcll(there & ((1ull << lane) - 1)) == at);
+        seq = __ffsll((unsigned long long)hit) - 1;
+        first = lo * kRows;
+        return true;
+    }
     int total = 0;
     for (int pass = 0; pass < 2; ++pass) {
         int before = 0;
         for (int b0 = 0; b0 < a.batch; b0 += 64) {
-            const int b = b0 + lane;
-            int n = 0;
-            if (b < a.batch) {
-                const long long rows = (long long)a.cu_q[b + 1] - a.cu_q[b];
-                if (rows > 0 && rows <= a.rows_q) n = (int)((rows * a.group + kRows - 1) / kRows);
-            }
+            const int n = blocks_of(a, b0 + lane);
             const int incl = wave_incl_sum(n);
             if (pass == 1) {
                 const uint64_t hit = __ballot(n > 0 && before + incl - n <= blk && blk < before + incl);
@@ -290,15 +312,16 @@ __global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a)
         if (tile + 1 < t_hi) fetch(tile + 1, lds[(tile + 1 - t_lo) & 1]);
         bool bad = false;
         if (masked) {
+            uint32_t carry = 0;
             // a value of v that is not finite must not meet the zero weight of a row that does not see it
 #pragma unroll
             for (int j = 0; j < NL; ++j) {
                 const uint4 c = *(const uint4*)(lv + (j * kThreads + tid) * 16);
-                const uint32_t u[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) bad |= not_finite<BF16>((uint16_t)u[i]) || not_finite<BF16>((uint16_t)(u[i] >> 16));
+                // all exponent bits set: adding the lowest of them carries into the sign's place
+                constexpr uint32_t e = BF16 ? 0x7f807f80u : 0x7c007c00u, low = BF16 ? 0x00800080u : 0x04000400u;
+                carry |= ((c.x & e) + low) | ((c.y & e) + low) | ((c.z & e) + low) | ((c.w & e) + low);
             }
-            bad = __syncthreads_or(bad);
+            bad = __syncthreads_or((carry & 0x80008000u) != 0);
         }
 
         acc s[NT];
@@ -312,11 +335,14 @@ __global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a)
             for (int t = 0; t < NT; ++t)
                 s[t] = mma<RW, BF16>(*(const s16x8*)(lk + k_at<D>(RW * t + m, KD / 8 * st + q)), qf[st], s[t]);
         if (masked) {
+            const int here = tile * kPos + 4 * q;
 #pragma unroll
-            for (int e = 0; e < NT * VE; ++e) {
-                const int p = tile * kPos + RW * (e / VE) + Sh::at(e % VE, q);
-                if (p > at || p < lo) s[e / VE][e % VE] = -__builtin_inff();
-            }
+            for (int e = 0; e < NT * VE; ++e)
+                if (RW * (e / VE) + Sh::at(e % VE, 0) > at - here) s[e / VE][e % VE] = -__builtin_inff();
+            if (a.window > 0)
+#pragma unroll
+                for (int e = 0; e < NT * VE; ++e)
+                    if (RW * (e / VE) + Sh::at(e % VE, 0) < lo - here) s[e / VE][e % VE] = -__builtin_inff();
         }
         float top = s[0][0];
 #pragma unroll
