@@ -756,16 +756,29 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
     const int t_lo = span_of(a, len, 0).lo >> 6, t_hi = (len + 63) >> 6;
     const float* lse = a.lse + ((long long)b * a.heads + head * a.group) * a.q_rows;
     float* weights = a.weights + ((long long)b * a.g.kv_heads + head) * a.w_stride;
-    for (int tile = t_lo + blockIdx.x * 4 + wave; tile < t_hi; tile += gridDim.x * 4) {
-        const long long at = kv::tile_at(a.g, tr, head, tile * 64);
-        if (at < 0) continue;
+    const int first = t_lo + blockIdx.x * 4 + wave, step = gridDim.x * 4;
+    for (int rb = 0; rb * 16 < rows && first < t_hi; ++rb) {
+        h16x8 qf[1][NW];
+        float factor[1], f[4], base[4];
+        Span sp[4];
         KTile<D> k;
-        load_k<D>(k, a.cache + at, c, q);
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int rb = 0; rb * 16 < rows; ++rb) {
-            h16x8 qf[1][NW];
-            float factor[1];
-            load_q<D, 1, BF16>(a, b, head, rb, c, q, qf, factor);
+        long long at = kv::tile_at(a.g, tr, head, first * 64);
+        load_k<D>(k, a.cache + (at < 0 ? 0 : at), c, q);
+        load_q<D, 1, BF16>(a, b, head, rb, c, q, qf, factor);
+        int all_lo = 0, all_hi = 0x7fffffff;               // positions that the lane's rows all see
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = rb * 16 + 4 * q + i;
+            f[i] = __shfl(factor[0], 4 * q + i);           // held by the lane whose c is the row
+            base[i] = r < rows ? -lse[r] : -__builtin_inff();
+            sp[i] = span_of(a, len, r);
+            if (r >= rows) continue;                       // rows that are not there weigh nothing
+            all_lo = sp[i].lo > all_lo ? sp[i].lo : all_lo;
+            all_hi = sp[i].hi < all_hi ? sp[i].hi : all_hi;
+        }
+        for (int tile = first; tile < t_hi; tile += step) {
+            const int next = tile + step;
+            const long long next_at = next < t_hi ? kv::tile_at(a.g, tr, head, next * 64) : -1;
             f32x4 s[4];
 #pragma unroll
             for (int bl = 0; bl < 4; ++bl) {
@@ -774,28 +787,30 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
                 for (int wd = 0; wd < NW; ++wd)
                     s[bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[0][wd], k_frag<D>(k, bl, wd), s[bl], 0, 0, 0);
             }
+            const bool there = at >= 0;
+            at = next_at;
+            if (next < t_hi) load_k<D>(k, a.cache + (at < 0 ? 0 : at), c, q);
+            if (!there) continue;
+            const int mine_at = tile * 64 + 16 * q + c;
+            const float old = mine_at < len ? weights[mine_at] : 0.0f;
+            float w[4] = {0.f, 0.f, 0.f, 0.f};
+            const bool whole = __ballot(tile * 64 < all_lo || tile * 64 + 64 > all_hi) == 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = rb * 16 + 4 * q + i;
-                const float f = __shfl(factor[0], 4 * q + i);     // held by the lane whose c is the row
-                const float base = r < rows ? -lse[r] : 0.0f;
-                const Span sp = span_of(a, len, r);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int bl = 0; bl < 4; ++bl) {
                     const int pos = tile * 64 + 16 * bl + c;
-                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[bl][i], f, base));
-                    w[bl] += pos >= sp.lo && pos < sp.hi ? e : 0.0f;
+                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[bl][i], f[i], base[i]));
+                    w[bl] += whole || (pos >= sp[i].lo && pos < sp[i].hi) ? e : 0.0f;
                 }
-            }
-        }
-        float mine = 0.0f;
+            float mine = 0.0f;
 #pragma unroll
-        for (int bl = 0; bl < 4; ++bl) {
-            const float t = sum_over_q(w[bl]);
-            mine = q == bl ? t : mine;
+            for (int bl = 0; bl < 4; ++bl) {
+                const float t = sum_over_q(w[bl]);
+                mine = q == bl ? t : mine;
+            }
+            if (mine_at < len) weights[mine_at] = old + mine;
         }
-        const int pos = tile * 64 + 16 * q + c;
-        if (pos < len) weights[pos] += mine;
     }
 }
 
@@ -873,8 +888,10 @@ static int launch(const Args& a, const Launch& p, int batch, int max_len, hipStr
     int rc = launch_status();
     if (rc != XP_OK || !a.weights) return rc;
     const long long tiles = ((long long)max_len + 63) / 64;
-    long long blocks = (tiles + 7) / 8;
-    blocks = blocks < 1 ? 1 : (blocks > 1024 ? 1024 : blocks);
+    // four waves a workgroup, three workgroups on each CU, at least a tile for each wave
+    long long blocks = (3 * kCus + (long long)batch * a.g.kv_heads - 1) / ((long long)batch * a.g.kv_heads);
+    blocks = blocks > (tiles + 3) / 4 ? (tiles + 3) / 4 : blocks;
+    blocks = blocks < 1 ? 1 : blocks;
     hipLaunchKernelGGL((attn_weights_kernel<D, BF16>), dim3((unsigned)blocks, a.g.kv_heads, batch), dim3(256), 0, s, a);
     return launch_status();
 }
