@@ -50,6 +50,7 @@ struct Args {
     int batch;
     int share, chunk;     // sequences longer than max(tiles of the batch / share, chunk) tiles are cut into pieces
     int waves;            // of a workgroup; pieces are whole rounds of them
+    bool in_order;        // no sequence is cut, and units follow the grid
     float scale_m;        // scale * log2(e) = scale_m * 2^scale_e
     int scale_e;
 };
@@ -97,10 +98,9 @@ __device__ __forceinline__ int dims_of(int q, int w) {
     return 128 * (w >> 2) + 32 * q + 8 * (w & 3);
 }
 
-// Query rows of a block of 16*MT as fp16 fragments, and each row's score factor.
-template <int D, int MT, bool BF16>
-__device__ __forceinline__ void load_q(const Args& a, int b, int head, int rb, int c, int q, h16x8 (&qf)[MT][Dim<D>::NW],
-                                       float (&factor)[MT]) {
+// Query rows of a block of 16*MT: as they are,
+template <int D, int MT>
+__device__ __forceinline__ void fetch_q(const Args& a, int b, int head, int rb, int c, int q, uint4 (&v)[MT][Dim<D>::NW]) {
     const int rows = a.q_rows * a.group;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -109,15 +109,22 @@ __device__ __forceinline__ void load_q(const Args& a, int b, int head, int rb, i
         const int tok = ok ? r / a.group : 0;
         const int hd = head * a.group + (ok ? r - tok * a.group : 0);
         const uint16_t* p = (const uint16_t*)a.q + ((long long)b * a.q_rows + tok) * a.q_stride + (long long)hd * D;
-        uint4 v[Dim<D>::NW];
 #pragma unroll
-        for (int w = 0; w < Dim<D>::NW; ++w) v[w] = ok ? *(const uint4*)(p + dims_of<D>(q, w)) : uint4{0, 0, 0, 0};
+        for (int w = 0; w < Dim<D>::NW; ++w) v[mt][w] = ok ? *(const uint4*)(p + dims_of<D>(q, w)) : uint4{0, 0, 0, 0};
+    }
+}
+// and as fp16 fragments, with each row's score factor.
+template <int D, int MT, bool BF16>
+__device__ __forceinline__ void make_q(const Args& a, const uint4 (&v)[MT][Dim<D>::NW], h16x8 (&qf)[MT][Dim<D>::NW],
+                                       float (&factor)[MT]) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
         int k = 0;
         if constexpr (BF16) {
             uint32_t top = 0;                   // exponent field of the row's largest magnitude
 #pragma unroll
             for (int w = 0; w < Dim<D>::NW; ++w) {
-                const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+                const uint32_t u[4] = {v[mt][w].x, v[mt][w].y, v[mt][w].z, v[mt][w].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t lo = (u[i] >> 7) & 255u, hi = (u[i] >> 23) & 255u;
@@ -132,7 +139,7 @@ __device__ __forceinline__ void load_q(const Args& a, int b, int head, int rb, i
             const float up = __uint_as_float((uint32_t)(127 + k) << 23);
 #pragma unroll
             for (int w = 0; w < Dim<D>::NW; ++w) {
-                const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+                const uint32_t u[4] = {v[mt][w].x, v[mt][w].y, v[mt][w].z, v[mt][w].w};
                 h16x8 f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -143,7 +150,7 @@ __device__ __forceinline__ void load_q(const Args& a, int b, int head, int rb, i
             }
         } else {
 #pragma unroll
-            for (int w = 0; w < Dim<D>::NW; ++w) qf[mt][w] = __builtin_bit_cast(h16x8, v[w]);
+            for (int w = 0; w < Dim<D>::NW; ++w) qf[mt][w] = __builtin_bit_cast(h16x8, v[mt][w]);
         }
         // kept a normal number: a masked -inf times 0, or a score of 0 times infinity, would be NaN
         factor[mt] = fminf(fmaxf(__builtin_amdgcn_ldexpf(a.scale_m, a.scale_e - k), 0x1p-126f), 0x1p127f);
@@ -323,19 +330,6 @@ __device__ __forceinline__ bool find_piece(const Args& a, int i, Piece& p) {
         return true;
     }
     // more sequences: their order is kept inside the cut and the whole ones
-    if (!a.share) {
-        if (JOIN || i >= (long long)a.batch * per) return false;
-        p.b = i / per;
-        p.unit = i - p.b * per;
-        p.len = length_of(a, p.b);
-        c = cut_of(a, p.len, limit);
-        p.pieces = 1;
-        p.slot = i;
-        p.tiles = p.each = c.tiles;
-        p.lo = c.lo;
-        p.index = 0;
-        return true;
-    }
     {
         long long all = 0;
         for (int b0 = 0; b0 < a.batch; b0 += 64) {
@@ -412,10 +406,30 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
 
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    // In order, units follow the grid: q and the first page are asked for before the length is known.
     Piece pc;
-    if (!find_piece<false>(a, blockIdx.x, pc)) return;
+    const int units = a.g.kv_heads * a.row_blocks, page_tiles = a.g.page >> 6;
+    int first_id = -1;
+    uint4 qv[MT][NW];
+    if (a.in_order) {
+        pc.b = blockIdx.x / units;
+        pc.unit = blockIdx.x - pc.b * units;
+        const int col = wave / page_tiles;
+        first_id = a.table[(long long)pc.b * a.g.max_pages + (col < a.g.max_pages ? col : 0)];
+        const int rb = pc.unit / a.g.kv_heads;
+        fetch_q<D, MT>(a, pc.b, pc.unit - rb * a.g.kv_heads, rb, c, q, qv);
+        pc.len = length_of(a, pc.b);
+        const Cut cut = cut_of(a, pc.len, 0x7fffffff);
+        pc.pieces = 1;
+        pc.slot = pc.index = 0;
+        pc.tiles = pc.each = cut.tiles;
+        pc.lo = cut.lo;
+    } else if (!find_piece<false>(a, blockIdx.x, pc)) {
+        return;
+    }
     const int b = pc.b, len = pc.len, rb = pc.unit / a.g.kv_heads, head = pc.unit - rb * a.g.kv_heads;
     const int32_t* tr = a.table + (long long)b * a.g.max_pages;
+    if (!a.in_order) fetch_q<D, MT>(a, b, head, rb, c, q, qv);
 
     // this piece's tiles, less those that no row of the block sees
     const int rows = a.q_rows * a.group, first_row = rb * MT * 16;
@@ -448,12 +462,13 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
     };
     // the next tile at or behind `tile` whose page exists (positions of others are not seen);
     // its page's column and its place on the page follow it
-    const int page_tiles = a.g.page >> 6;
     const long long tile_bytes = kv::tile_bytes(NG);
+    bool asked = a.in_order && t0 == 0;
     int tile = t0 + wave, col = tile / page_tiles, in_page = tile - col * page_tiles;
     auto find = [&](int& tile) {
         for (; tile < t1; tile += waves) {
-            const int id = tr[col];
+            const int id = asked ? first_id : tr[col];
+            asked = false;
             const long long at = (((long long)id * a.g.kv_heads + head) * page_tiles + in_page) * tile_bytes;
             for (in_page += waves; in_page >= page_tiles; in_page -= page_tiles) ++col;
             if ((unsigned)id < (unsigned)a.g.n_pages) return a.cache + at;
@@ -467,7 +482,7 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
     }
     h16x8 qf[MT][NW];
     float factor[MT];
-    load_q<D, MT, BF16>(a, b, head, rb, c, q, qf, factor);
+    make_q<D, MT, BF16>(a, qv, qf, factor);
 
     f32x4 o[MT][NH];
     float m[MT], l[MT];
@@ -764,7 +779,9 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
         KTile<D> k;
         long long at = kv::tile_at(a.g, tr, head, first * 64);
         load_k<D>(k, a.cache + (at < 0 ? 0 : at), c, q);
-        load_q<D, 1, BF16>(a, b, head, rb, c, q, qf, factor);
+        uint4 qv[1][NW];
+        fetch_q<D, 1>(a, b, head, rb, c, q, qv);
+        make_q<D, 1, BF16>(a, qv, qf, factor);
         int all_lo = 0, all_hi = 0x7fffffff;               // positions that the lane's rows all see
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -947,6 +964,8 @@ XP_API int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows,
     a.batch = batch;
     a.share = p.share;
     a.waves = p.waves;
+    // units that each have a CU, or of more sequences than a wave sorts, need no order
+    a.in_order = !p.share && (p.units <= kCus || batch > 64);
     a.chunk = p.chunk;
     a.window = window;
     a.scale_m = (float)__builtin_frexp((double)scale * 1.4426950408889634, &a.scale_e);
