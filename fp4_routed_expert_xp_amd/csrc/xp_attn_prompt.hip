@@ -29,6 +29,7 @@ typedef __attribute__((ext_vector_type(8))) _Float16 h16x8;
 typedef __attribute__((ext_vector_type(8))) __bf16 b16x8;
 typedef __attribute__((ext_vector_type(8))) short s16x8;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(2))) short s16x2;
 
 typedef __attribute__((address_space(3))) void* lptr;
 typedef __attribute__((address_space(1))) const void* gptr;
@@ -74,6 +75,18 @@ template <bool BF16>
 __device__ __forceinline__ short half_of(float x) {
     if constexpr (BF16) return __builtin_bit_cast(short, (__bf16)x);
     return __builtin_bit_cast(short, (_Float16)x);
+}
+
+// c + the two halves of a pair.
+template <bool BF16>
+__device__ __forceinline__ float plus_pair(s16x2 a, float c) {
+    if constexpr (BF16) {
+        typedef __attribute__((ext_vector_type(2))) __bf16 b16x2;
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b16x2, a), b16x2{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+    } else {
+        typedef __attribute__((ext_vector_type(2))) _Float16 h16x2;
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(h16x2, a), h16x2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+    }
 }
 
 template <bool BF16>
@@ -359,15 +372,18 @@ __global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a)
             for (int d = 0; d < ND; ++d) o[d] *= alpha;
         }
         const float base = mx == -__builtin_inff() ? 0.0f : -mx;
+        // The sum is of the rounded exponentials, two at a time: what rounding adds to a weight
+        // that stands out it adds to the sum as well (a maximum that lags is not 1 exactly).
         s16x8 p[NT * VE / 8];
-        float add = 0.0f;
 #pragma unroll
-        for (int e = 0; e < NT * VE; ++e) {
+        for (int e = 0; e < NT * VE; e += 2) {
             const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e / VE][e % VE], a.scale_log2, base));
-            add += x;
-            p[e >> 3][e & 7] = half_of<BF16>(x);
+            const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[(e + 1) / VE][(e + 1) % VE], a.scale_log2, base));
+            const s16x2 xy = s16x2{half_of<BF16>(x), half_of<BF16>(y)};
+            p[e >> 3][e & 7] = xy.x;
+            p[e >> 3][(e & 7) + 1] = xy.y;
+            sum = plus_pair<BF16>(xy, sum);
         }
-        sum += add;
 
         if (masked && bad) {
             set_apart<D, RW, BF16>(o, lv, tile * kPos, at, lo);

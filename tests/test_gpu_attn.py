@@ -551,6 +551,9 @@ def check_prompt(q, k, v, cu_q, cu_k, out, scale, window=0):
             inf = np.isinf(want)
             assert np.array_equal(want[inf], got[inf]), (b, h)
             ok = np.isfinite(want)
+            # The weights are rounded by e (|e| <= p_step) in the products and in their sum: the output is off by
+            # sum p e (v - out), at most p_step (sum p |v| + |out|); the bound so far holds the first part
+            tol = tol + HALF[q.dtype] * np.abs(want)
             # fp16 probabilities below its normal range round by up to 2^-25
             tol = tol + FLOOR[q.dtype] * (1.0 + np.abs(np.where(np.isfinite(vv), vv, 0.0)).sum(0)[None, :])
             err = np.abs(got - want)
