@@ -439,7 +439,7 @@ XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int
         return XP_ERR_SHAPE;
     const int group = heads / kv_heads;
     const int64_t blocks = ((int64_t)rows_q * group + kRows - 1) / kRows + batch;
-    if ((int64_t)rows_q * group > 0x7fffffff - kRows || rows_k > 0x7fffffff - kPos || blocks * kv_heads > 0x7fffffff)
+    if ((int64_t)rows_q * group > 0x7fffffff - kRows || rows_k > 0x7fffffff - kPos || blocks * kv_heads >= (1 << 23))   // a launch has fewer than 2^32 threads
         return XP_ERR_SHAPE;
     if (batch == 0 || rows_q == 0) return XP_OK;
     if (!q || !cu_q || !cu_k || !out || (rows_k > 0 && (!k || !v))) return XP_ERR_NULL;

@@ -477,7 +477,7 @@ static int check_rows(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, 
                       const void* cache) {
     const int st = check_geo(dims, batch, max_pages);
     if (st != XP_OK) return st;
-    if (rows < 0 || rows > 0x7fffffff - 64 || (int64_t)rows * dims->kv_heads > 0xffffffffLL || type < XP_BF16 || type > XP_F32)
+    if (rows < 0 || rows > 0x7fffffff - 64 || (int64_t)rows * dims->kv_heads >= (1 << 30) || type < XP_BF16 || type > XP_F32)
         return XP_ERR_SHAPE;
     if (rows == 0 || batch == 0) return XP_OK;
     if (!k || !v || !cu || !start || !table || !cache) return XP_ERR_NULL;

@@ -381,7 +381,8 @@ int xp_kv_append(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32
 
 /* The reverse, for the same row map: the cached values as `type` (any xp_type; all
  * three hold them exactly). Rows whose position the cache does not have are 0; rows
- * from cu_rows[batch] on are left as they were. A prompt's next piece reads its
+ * from cu_rows[batch] on are left as they were. rows * kv_heads is below 2^30 for both
+ * calls. A prompt's next piece reads its
  * prefix back with it for xp_attn_prompt. */
 int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, int32_t type,
                const int32_t* cu_rows, const int32_t* start, const int32_t* table, const uint8_t* cache, void* k,
@@ -428,7 +429,8 @@ size_t xp_attn_decode_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int
  * weights (or NULL): fp32 [batch][kv_heads] rows of w_stride >= max_pages * page; the
  * call adds to each position the probabilities of all the kv head's rows there.
  * workspace: 16-byte aligned, needs no initial value; calls that share it must not
- * overlap. Results do not depend on the launch's timing. */
+ * overlap. Results do not depend on the launch's timing. heads * q_rows is at most 2^24,
+ * batch times the kv heads' blocks of 16 rows at most 2^22. */
 int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_t batch, int32_t max_pages,
                    int32_t max_len, int32_t type, const void* q, int64_t q_stride, float scale, int32_t window,
                    const uint8_t* cache, const int32_t* table, const int32_t* lens, void* out, int64_t out_stride,
@@ -441,7 +443,7 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
  * Its last query sits at its last key's position, so a prompt's later piece may
  * attend to the earlier pieces' keys; a query before its first key sees nothing.
  * Rows of out from cu_q[batch] on are left as they were. Strides of k and v are below
- * 2^24 elements. */
+ * 2^24 elements, rows_q * heads below 2^29. */
 int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch, int32_t rows_q, int32_t rows_k,
                    int32_t type, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                    int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, float scale, int32_t window, void* out,

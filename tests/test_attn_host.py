@@ -63,7 +63,7 @@ def test_row_calls_refuse(name):
     for key in ("k", "v", "cu", "start", "table", "cache"):
         assert call(**{key: None}) == xp.XP_ERR_NULL, key
     for kw in (dict(batch=-1), dict(batch=65536), dict(cols=0), dict(rows=-1), dict(ty=3), dict(ty=-1),
-               dict(ks=120), dict(vs=64), dict(ks=132), dict(vs=129), dict(ty=F32, ks=130), dict(cols=1 << 26),
+               dict(rows=1 << 29), dict(ks=120), dict(vs=64), dict(ks=132), dict(vs=129), dict(ty=F32, ks=130), dict(cols=1 << 26),
                dict(k=ODD), dict(v=ODD), dict(cache=ODD), dict(cu=ctypes.c_void_p(0x1002)),
                dict(table=ctypes.c_void_p(0x1001)), dict(start=ctypes.c_void_p(0x1002))):
         assert call(**kw) == xp.XP_ERR_SHAPE, kw
@@ -92,7 +92,7 @@ def test_decode_refuses():
                dict(os=252), dict(qs=260), dict(os=258), dict(q=ODD), dict(out=ODD), dict(cache=ODD), dict(work=ODD),
                dict(lens=ctypes.c_void_p(0x1002)), dict(table=ctypes.c_void_p(0x1002)),
                dict(weights=P, ws=63), dict(weights=ctypes.c_void_p(0x1002), ws=64),
-               dict(heads=65534, q_rows=65535, qs=1 << 30, os=1 << 30)):
+               dict(heads=65534, q_rows=65535, qs=1 << 30, os=1 << 30), dict(batch=65535, q_rows=4096)):
         assert _decode(**kw) == xp.XP_ERR_SHAPE, kw
     assert _decode(batch=0, q=None, cache=None, table=None, lens=None, out=None, work=None, bytes=0) == xp.XP_OK
     need = xp.xp_attn_decode_workspace_bytes(xp.kv_dims(2, 64, 64, 4), 4, 1, 1, 4096)
@@ -133,7 +133,7 @@ def test_prompt_refuses():
                dict(batch=-1), dict(batch=65536), dict(rq=-1), dict(rk=-1), dict(ty=F32), dict(ty=-1), dict(window=-1),
                dict(scale=0.0), dict(scale=-2.0), dict(scale=inf), dict(scale=nan), dict(qs=248), dict(ks=120), dict(vs=120),
                dict(os=248), dict(ks=1 << 24), dict(vs=1 << 24), dict(qs=258), dict(ks=132), dict(vs=130), dict(os=258), dict(q=ODD), dict(k=ODD), dict(v=ODD),
-               dict(out=ODD), dict(cq=ctypes.c_void_p(0x1002)), dict(rq=0x7fffffff), dict(rk=0x7fffffff)):
+               dict(out=ODD), dict(cq=ctypes.c_void_p(0x1002)), dict(rq=1 << 28), dict(rq=0x7fffffff), dict(rk=0x7fffffff)):
         assert call(**kw) == xp.XP_ERR_SHAPE, kw
     assert call(rq=0, q=None, out=None) == xp.XP_OK
     assert call(batch=0, q=None, k=None, v=None, cq=None, ck=None, out=None) == xp.XP_OK
