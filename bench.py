@@ -53,6 +53,11 @@ PF_DN_TRAFFIC = dict(sources="228f5abb", fetch_kib=865250.3, write_kib=524458.8)
 PREFILL_SOURCES = ("xp_prefill.hip", "xp_prefill_asm.h", "xp_common.h")
 
 
+# The attention cell (not among the default cells): rows of a step, positions of each row's
+# sequence, rows of a prompt chunk.
+ATTN_ROWS, ATTN_CONTEXT, ATTN_PROMPT_ROWS = (1, 16), 8192, 4096
+
+
 def csrc_digest(sources=ROOFLINE_SOURCES) -> str:
     """Digest of a kernel's sources (its .hip file and the internal headers it includes)."""
     import hashlib
@@ -450,6 +455,77 @@ class Fp8Cell:
         torch.cuda.synchronize()
 
 
+class AttnCell:
+    """A decode layer's attention (the "attention" cell): 32 heads of 128 over 8 kv heads, one
+    4-bit cache per layer holding ATTN_CONTEXT positions for each row's sequence (seeded codes)."""
+    HEADS, KV, DIM, PAGE = 32, 8, 128, 256
+
+    def __init__(self, layers: int, rows: int):
+        import torch
+        from fp4_routed_expert_xp_amd import xp
+        self.layers, self.rows = layers, rows
+        self.cols = ATTN_CONTEXT // self.PAGE
+        self.d = xp.kv_dims(self.KV, self.DIM, self.PAGE, rows * self.cols)
+        g = torch.Generator(device="cuda").manual_seed(6001)
+        nbytes, tile = xp.xp_kv_bytes(self.d), self.DIM // 32 * 2176
+        one = torch.randint(0, 256, (nbytes // tile, tile), generator=g, device="cuda", dtype=torch.uint8)
+        for at in (self.DIM // 32 * 1024, self.DIM // 32 * 2112):       # scales of 1/4 .. 1/2
+            one[:, at:at + self.DIM * 2] = torch.randint(0x28, 0x31, (nbytes // tile, self.DIM * 2), generator=g,
+                                                         device="cuda", dtype=torch.uint8)
+        self.caches = [one.view(-1).clone() for _ in range(layers)]
+        self.table = torch.randperm(rows * self.cols, generator=g, device="cuda").to(torch.int32).view(rows, self.cols)
+        self.start = torch.full((rows,), ATTN_CONTEXT - 1, dtype=torch.int32, device="cuda")
+        self.lens = self.start + 1
+        self.cu = torch.arange(rows + 1, dtype=torch.int32, device="cuda")
+        self.q = torch.randn(rows, self.HEADS, self.DIM, generator=g, device="cuda").to(torch.bfloat16)
+        self.k, self.v = (torch.randn(rows, self.KV, self.DIM, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv")
+        self.out = torch.empty_like(self.q)
+        self.ws = torch.empty(xp.xp_attn_decode_workspace_bytes(self.d, self.HEADS, 1, rows, ATTN_CONTEXT),
+                              dtype=torch.uint8, device="cuda")
+
+    def step(self, layer: int) -> None:
+        from fp4_routed_expert_xp_amd import xp
+        xp.xp_kv_append(self.d, self.k, self.v, self.cu, self.start, self.table, self.caches[layer])
+        xp.xp_attn_decode(self.d, self.q, self.caches[layer], self.table, self.lens, ATTN_CONTEXT, self.DIM ** -0.5,
+                          self.out, self.ws)
+
+
+def time_attn(layers: int, steps: int, warmup: int) -> dict:
+    """Per row count: one graph of every layer's append and attention; and one prompt chunk's attention."""
+    import torch
+    from fp4_routed_expert_xp_amd import xp
+    out = {}
+    for rows in ATTN_ROWS:
+        cell = AttnCell(layers, rows)
+        cell.step(0)
+        torch.cuda.synchronize()
+        g = _graph(lambda: [cell.step(l) for l in range(layers)])
+        for _ in range(warmup):
+            g.replay()
+        torch.cuda.synchronize()
+        ms = _replay_ms(g, steps)
+        us = ms * 1e3 / layers
+        nbytes = rows * ATTN_CONTEXT * cell.KV * cell.DIM * 17 // 16
+        out["attention/%d" % rows] = dict(
+            rows=rows, context=ATTN_CONTEXT, round_ms=round(ms, 4), layer_us=round(us, 3), cache_bytes=nbytes,
+            cache_gbps=round(nbytes / us / 1e3, 1), pct_hbm_peak=round(nbytes / us / 1e1 / HBM_PEAK_GBPS, 2))
+        del g, cell
+    n, c = ATTN_PROMPT_ROWS, AttnCell
+    q = torch.randn(n, c.HEADS, c.DIM, device="cuda").to(torch.bfloat16)
+    k, v = (torch.randn(n, c.KV, c.DIM, device="cuda").to(torch.bfloat16) for _ in "kv")
+    o, cu = torch.empty_like(q), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    xp.xp_attn_prompt(q, k, v, cu, cu, c.DIM ** -0.5, o)
+    torch.cuda.synchronize()
+    g = _graph(lambda: xp.xp_attn_prompt(q, k, v, cu, cu, c.DIM ** -0.5, o))
+    for _ in range(warmup):
+        g.replay()
+    torch.cuda.synchronize()
+    us = _replay_ms(g, steps) * 1e3
+    out["attention/prompt"] = dict(rows=n, us=round(us, 2),
+                                   tflops=round(2 * n * (n + 1) * c.HEADS * c.DIM / us / 1e6, 1))
+    return out
+
+
 def time_fp8(cell: Fp8Cell, steps: int, warmup: int) -> dict:
     """Per row count: the round (every projection of every layer, one graph) and
     each shape alone (a graph of that shape over the layers)."""
@@ -630,6 +706,11 @@ def main():
     log("plain copy bandwidth %.0f GB/s" % copy_gbps)
     reports, timings = {}, {}
     for name in cells:
+        if name == "attention":
+            for key, rep in time_attn(args.layers, args.steps, args.warmup).items():
+                reports[key] = rep
+                log("%s: %s" % (key, json.dumps(rep)))
+            continue
         if name == "fp8_rows":
             fcell = Fp8Cell(args.layers)
             for R, rep in time_fp8(fcell, args.steps, args.warmup).items():
@@ -675,7 +756,7 @@ def main():
                 rep["tiers"] = {"gate_up": list(gu), "down": list(dn)}
                 reports[key] = rep
                 log("%s: %s" % (key, json.dumps(rep)))
-    decode = [c for c in cells if c not in ("prefill", "fp8_rows")]
+    decode = [c for c in cells if c not in ("prefill", "fp8_rows", "attention")]
     if not decode:
         log("the headline is a decode workload: name one of one_row, four_same, sixteen_random in --cells")
         sys.exit(2)
