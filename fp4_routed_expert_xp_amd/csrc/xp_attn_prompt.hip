@@ -13,10 +13,13 @@
 //
 // Waves of 32 rows read k and v from LDS half as often; their registers (outputs,
 // scores, q) leave two waves a SIMD up to 128 columns and one at 256, where waves of 16
-// rows leave two: 8 heads of 256 over 4,096 rows take 157 us in those and 233 us in
-// waves of 32, 32 heads of 128 over 8,192 rows 635 us in waves of 16 and 581 us in 32.
-// Bound there by the matrix pipes (44% busy) and the vector pipes (46%, the
-// exponentials most of it), which overlap for a sixth of the time.
+// rows leave two: 8 heads of 256 over 4,096 rows take 155 us in those and 233 us in
+// waves of 32, 32 heads of 128 over 8,192 rows 635 us in waves of 16 and 590 us in 32
+// (930 TFLOP/s of the pairs that are seen; a large bf16 product runs at 1,380 here).
+// Bound there by both pipes in turn: of the SIMDs' time the matrix pipe is busy 42%,
+// the vector pipe 38% (the exponentials two fifths of it), both at once 10%; the rest
+// is waiting at the barrier of each tile and for LDS. LDS itself is busy 21%, without
+// bank conflicts.
 //
 // Scores, maxima, sums and outputs are fp32; exponentials round once to the type of
 // v (the product's operand), the result once to the output type.

@@ -164,7 +164,9 @@ __global__ __launch_bounds__(256) void read_row_kernel(Geo g, RowMap m, const ui
 // Many rows: a workgroup takes 64 rows of one kv head, so that the lines of a tile are
 // written and read by one workgroup (or two, where rows and tiles are not aligned) and
 // not by several chip parts with an L2 each. Bound by bytes: 2 (or 4) a value on one
-// side, 4.25 bits on the other.
+// side, 4.25 bits on the other: 8,214 fp32 rows of 8 heads of 128 go in within 23 to
+// 25 us (76 MB, 3.2 TB/s) and come out as bf16 in 12 us (43 MB, 3.5 TB/s); 32,768 rows
+// come out in 30 us (170 MB, 5.6 TB/s). A workgroup for each row took 25, 18 and 60 us.
 constexpr int kBlockRows = 64;
 constexpr int kBatchRows = 4;   // rows a thread has in flight
 struct Block {
@@ -257,6 +259,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // of 12, 10 and 10 bits: the first takes sign, exponent and three bits of the
 // significand, so weights that fall off over many powers of two spread over its bins.
 // Then each wave walks its own run of positions, once to count and once to write.
+// Bound by its own steps: 26 us for 64 of them over up to 16,384 positions (four passes
+// of eight bits over keys in memory took 36 us), 10 us for eight over 1,100.
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(Geo g, const int32_t* __restrict__ lens,
                                                                    const float* weights, long long w_stride, int keep,
                                                                    int sinks, int recent, int32_t* kept,
@@ -391,7 +395,9 @@ constexpr int kMoveSteps = 4;
 // positions' codes and scale bytes, in order. As above a step's loads are done
 // before its stores, and later steps read only behind them, so the destination
 // pages may be the source's own. Bound by bytes (17 in and out a position) and,
-// for few positions, by the chain kept -> page table -> bytes of each step.
+// for few positions, by the chain kept -> page table -> bytes of each step: a batch cut
+// to a quarter takes 33 to 38 us, for the kept positions lie in most of the source's
+// lines (103 MB fetched for 36 MB kept, and 36 MB written).
 __global__ __launch_bounds__(kMoveThreads) void evict_move_kernel(Geo src, Geo dst, const int32_t* lens,
                                                                   const int32_t* __restrict__ table,
                                                                   const int32_t* __restrict__ dst_table,
