@@ -490,27 +490,34 @@ def _refuse(t, dtype, name: str, numel: int, dev: int) -> None:
 
 
 def _arg(t, dtype, name: str, numel: int, dev: int) -> int:
-    """Address of a contiguous tensor of at least numel elements on device dev."""
+    """Address of a contiguous tensor of at least numel elements on device dev (-1: none)."""
     if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or dev < 0
             or t.numel() < numel or not t.is_contiguous()):
         _refuse(t, dtype, name, numel, dev)
     return t.data_ptr()
 
 
-def _rows3(t, dtype, name: str, rows: int, heads: int, dim: int, dev: int):
-    """A device tensor [rows][heads][dim] whose rows may lie apart: (address, stride between rows)."""
+def _refuse_rows(t, dtype, name: str, shape, dev: int) -> None:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
     if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != (rows, heads, dim):
-        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, dim, list(t.shape)))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if t.get_device() != dev:
-        _refuse(t, dtype, name, 0, dev)
-    st = t.stride()
-    if (st[2] != 1 or (st[1] != dim and heads > 1)) and t.numel():
-        raise ValueError("%s: a row's heads must be contiguous" % name)
-    return t.data_ptr(), (st[0] if rows > 1 else heads * dim)
+        _refuse(t.contiguous(), dtype, name, 0, dev)
+    raise ValueError("%s: a row's heads must be contiguous" % name)
+
+
+def _rows3(t, dtype, name: str, shape, dev: int):
+    """A device tensor of shape (rows, heads, dim) whose rows may lie apart: (address, stride between rows)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0:
+        _refuse_rows(t, dtype, name, shape, dev)
+    row, head, one = t.stride()
+    rows, heads, dim = shape
+    if (one != 1 or (head != dim and heads > 1)) and rows > 0:
+        _refuse_rows(t, dtype, name, shape, dev)
+    return t.data_ptr(), (row if rows > 1 else heads * dim)
 
 
 def _table(t, name: str, dev: int):
@@ -523,13 +530,14 @@ def _table(t, name: str, dev: int):
 
 
 def _type(t, name: str, types) -> int:
-    dt = getattr(t, "dtype", None)
-    if dt not in types:
+    """The xp_type of a tensor, one of types."""
+    ty = types.get(getattr(t, "dtype", None))
+    if ty is None:
         raise ValueError("%s must be one of %s" % (name, ", ".join(str(x) for x in types)))
-    return XP_TYPES[dt]
+    return ty
 
 
-_HALVES = (torch.bfloat16, torch.float16)
+_HALVES = {torch.bfloat16: 0, torch.float16: 1}
 
 
 def _weights(w, name: str, batch: int, kv_heads: int, least: int, dev: int):
@@ -563,9 +571,9 @@ def xp_kv_append(d: xp_kv_dims, k, v, cu_rows, start, table, cache, stream=None)
     """Quantise the packed rows k, v [rows][kv_heads][head_dim] into the cache (see xp.h)."""
     ty, dev, heads, dim = _type(k, "k", XP_TYPES), k.get_device(), d.kv_heads, d.head_dim
     tp, batch, cols = _table(table, "table", dev)
-    rows = k.shape[0]
-    kp, ks = _rows3(k, k.dtype, "k", rows, heads, dim, dev)
-    vp, vs = _rows3(v, k.dtype, "v", rows, heads, dim, dev)
+    rows, dt = k.shape[0], k.dtype
+    kp, ks = _rows3(k, dt, "k", (rows, heads, dim), dev)
+    vp, vs = _rows3(v, dt, "v", (rows, heads, dim), dev)
     _launch(lib().xp_kv_append, "xp_kv_append", dev, stream,
             (ctypes.byref(d), batch, cols, rows, ty, kp, ks, vp, vs, _arg(cu_rows, torch.int32, "cu_rows", batch + 1, dev),
              _arg(start, torch.int32, "start", batch, dev), tp, _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev)))
@@ -575,9 +583,9 @@ def xp_kv_read(d: xp_kv_dims, cu_rows, start, table, cache, k, v, stream=None) -
     """Read cached rows back into k, v [rows][kv_heads][head_dim] (see xp.h)."""
     ty, dev, heads, dim = _type(k, "k", XP_TYPES), k.get_device(), d.kv_heads, d.head_dim
     tp, batch, cols = _table(table, "table", dev)
-    rows = k.shape[0]
-    kp, ks = _rows3(k, k.dtype, "k", rows, heads, dim, dev)
-    vp, vs = _rows3(v, k.dtype, "v", rows, heads, dim, dev)
+    rows, dt = k.shape[0], k.dtype
+    kp, ks = _rows3(k, dt, "k", (rows, heads, dim), dev)
+    vp, vs = _rows3(v, dt, "v", (rows, heads, dim), dev)
     _launch(lib().xp_kv_read, "xp_kv_read", dev, stream,
             (ctypes.byref(d), batch, cols, rows, ty, _arg(cu_rows, torch.int32, "cu_rows", batch + 1, dev),
              _arg(start, torch.int32, "start", batch, dev), tp, _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev),
@@ -612,8 +620,9 @@ def xp_attn_decode(d: xp_kv_dims, q, cache, table, lens, max_len: int, scale: fl
     ty, dev, q_rows = _type(q, "q", _HALVES), q.get_device(), int(q_rows)
     tp, batch, cols = _table(table, "table", dev)
     heads, dim = q.shape[1] if q.dim() == 3 else 0, d.head_dim
-    qp, qs = _rows3(q, q.dtype, "q", batch * q_rows, heads, dim, dev)
-    op, os_ = _rows3(out, q.dtype, "out", batch * q_rows, heads, dim, dev)
+    shape = (batch * q_rows, heads, dim)
+    qp, qs = _rows3(q, q.dtype, "q", shape, dev)
+    op, os_ = _rows3(out, q.dtype, "out", shape, dev)
     wp, ws = (0, 0) if weights is None else _weights(weights, "weights", batch, d.kv_heads, cols * d.page, dev)
     _launch(lib().xp_attn_decode, "xp_attn_decode", dev, stream,
             (ctypes.byref(d), heads, q_rows, batch, cols, int(max_len), ty, qp, qs, scale, int(window),
@@ -629,10 +638,11 @@ def xp_attn_prompt(q, k, v, cu_q, cu_k, scale: float, out, window: int = 0, stre
         raise ValueError("q and k must be [rows][heads][head_dim]")
     rows_q, heads, dim = q.shape
     rows_k, kv_heads, _ = k.shape
-    qp, qs = _rows3(q, q.dtype, "q", rows_q, heads, dim, dev)
-    kp, ks = _rows3(k, q.dtype, "k", rows_k, kv_heads, dim, dev)
-    vp, vs = _rows3(v, q.dtype, "v", rows_k, kv_heads, dim, dev)
-    op, os_ = _rows3(out, q.dtype, "out", rows_q, heads, dim, dev)
+    dt, shape = q.dtype, (rows_k, kv_heads, dim)
+    qp, qs = _rows3(q, dt, "q", (rows_q, heads, dim), dev)
+    kp, ks = _rows3(k, dt, "k", shape, dev)
+    vp, vs = _rows3(v, dt, "v", shape, dev)
+    op, os_ = _rows3(out, dt, "out", (rows_q, heads, dim), dev)
     cq = _arg(cu_q, torch.int32, "cu_q", 1, dev)
     seqs = cu_q.numel()
     _launch(lib().xp_attn_prompt, "xp_attn_prompt", dev, stream,
