@@ -219,7 +219,7 @@ __device__ __forceinline__ Span span_of(const Args& a, int len, int r) {
     const int at = len - a.q_rows + r / a.group;          // the row's own position
     Span s;
     s.hi = r < rows ? at + 1 : 0;
-    s.lo = a.window > 0 && at - a.window + 1 > 0 ? at - a.window + 1 : 0;
+    s.lo = kv::first_seen(at, a.window);
     return s;
 }
 

@@ -267,7 +267,7 @@ __global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a)
     const int tok = live ? row / a.group : 0;
     const int hd = head * a.group + (live ? row - tok * a.group : 0);
     const int at = live ? tok + shift : -1;    // the row's own position
-    const int lo = a.window > 0 && at - a.window + 1 > 0 ? at - a.window + 1 : 0;
+    const int lo = kv::first_seen(at, a.window);
 
     s16x8 qf[NS];
     const uint16_t* qp = a.q + (long long)(q0 + tok) * a.q_stride + (long long)hd * D + 8 * q;
@@ -278,9 +278,8 @@ __global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a)
     const int last_row = first + kRows < rows ? first + kRows - 1 : rows - 1;
     const int at_first = first / a.group + shift, at_last = last_row / a.group + shift;
     const int t_hi = at_last >= 0 ? (at_last >> 6) + 1 : 0;
-    const int w_first = at_first - a.window + 1, w_last = at_last - a.window + 1;
-    const int t_lo = a.window > 0 && w_first > 0 ? w_first >> 6 : 0;
-    const int full_lo = a.window > 0 && w_last > 0 ? w_last : 0, full_hi = at_first + 1;
+    const int t_lo = kv::first_seen(at_first, a.window) >> 6;
+    const int full_lo = kv::first_seen(at_last, a.window), full_hi = at_first + 1;
 
     acc o[ND];
 #pragma unroll

@@ -52,6 +52,11 @@ __device__ __forceinline__ int v_scale(int groups, int pos, int g) {
     return groups * 2112 + g * 64 + ((pos >> 2) & 3) * 16 + (pos >> 4) * 4 + (pos & 3);
 }
 
+// The first position that a row at position `at` sees: any window up to 2^31 - 1, any at.
+__device__ __forceinline__ int first_seen(int at, int window) {
+    return window > 0 && at >= window ? at - window + 1 : 0;
+}
+
 __device__ __forceinline__ float e4m3_value(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0); }
 
 // The smallest E4M3FN scale s with 6 s >= amax (amax >= 0), 448 when there is

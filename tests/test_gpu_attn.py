@@ -234,6 +234,27 @@ def test_decode_ragged_batches(batch, max_len):
     check_decode(c, table, lens, q, out, 0.125, q_rows=2)
 
 
+def test_windows_as_wide_as_an_int():
+    """A window of 2^31 - 1 is none, also where queries lie before the first key."""
+    rng = np.random.default_rng(77)
+    c = filled(rng, 1, 64, 64, 8)
+    table = tables(rng, 4, 2, 8)
+    lens = np.array([1, 3, 7, 100], dtype=np.int32)
+    q = dev(rng.normal(size=(4 * 6, 2, 64)), torch.bfloat16)
+    buf = on_device(c)
+    out = run_decode(c, buf, table, lens, q, 0.125, 2 ** 31 - 1, 6)
+    check_decode(c, table, lens, q, out, 0.125, 0, 6)
+    assert torch.equal(out, run_decode(c, buf, table, lens, q, 0.125, 0, 6))
+    cu_q, cu_k = ends([9, 70]), ends([2, 70])
+    q = dev(rng.normal(size=(79, 2, 64)), torch.float16)
+    k, v = (dev(rng.normal(size=(72, 1, 64)), torch.float16) for _ in "kv")
+    out, none = torch.empty_like(q), torch.empty_like(q)
+    xp.xp_attn_prompt(q, k, v, dev(cu_q), dev(cu_k), 0.125, out, window=2 ** 31 - 1)
+    xp.xp_attn_prompt(q, k, v, dev(cu_q), dev(cu_k), 0.125, none)
+    check_prompt(q, k, v, cu_q, cu_k, out, 0.125)
+    assert torch.equal(out, none)
+
+
 def test_decode_lengths_out_of_range_are_clamped():
     rng = np.random.default_rng(8)
     c = filled(rng, 2, 64, 64, 6)
