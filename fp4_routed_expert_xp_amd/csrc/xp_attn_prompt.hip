@@ -3,7 +3,7 @@
 //
 // One pass over the keys with a running maximum and sum. A row is a (token, head of
 // the kv head's group) pair, tokens first, so the heads that share keys share a
-// workgroup and a short prompt still fills its 128 rows. A wave owns RW rows and takes
+// workgroup and a short prompt still fills its rows. A wave owns RW rows and takes
 // 64 positions at a time. S^T = K Q^T (v_mfma_f32_32x32x16 for 32 rows, 16x16x32 for
 // 16; positions as the matrix rows) leaves lane (m, q) = (lane % RW, lane / RW) with
 // row m at every fourth quad of positions, so the exponentials, once rounded, are the
@@ -37,8 +37,12 @@ typedef __attribute__((ext_vector_type(2))) short s16x2;
 typedef __attribute__((address_space(3))) void* lptr;
 typedef __attribute__((address_space(1))) const void* gptr;
 
-constexpr int kRows = 128;   // rows of a workgroup
 constexpr int kPos = 64;     // positions of a tile
+// Up to this many workgroups of 128 rows (two for each CU) they are of 64 rows, in waves
+// of 16: each CU's chain of tiles is shorter. 2,000 rows of 16/8 heads of 128 (264
+// workgroups) take 48 us so and 58 us in 128 rows, 1,000 of 32/8 28 and 33; 2,000 of
+// 32/8 (512) 58 and 60; eight packed prompts to 1,000 (1,190) 83 and 61.
+constexpr int kFew = 512;
 constexpr float kLag = 8.0f; // of the running maximum, in powers of two
 
 struct Args {
@@ -180,19 +184,21 @@ __device__ __forceinline__ void set_apart(typename Shape<RW>::acc (&o)[D / RW], 
         }
 }
 
+template <int ROWS>
 __device__ __forceinline__ int blocks_of(const Args& a, int b) {
     if (b >= a.batch) return 0;
     const long long rows = (long long)a.cu_q[b + 1] - a.cu_q[b];
-    return rows > 0 && rows <= a.rows_q ? (int)((rows * a.group + kRows - 1) / kRows) : 0;
+    return rows > 0 && rows <= a.rows_q ? (int)((rows * a.group + ROWS - 1) / ROWS) : 0;
 }
 // The workgroup's block of rows: sequence and first row. The blocks that run longest,
 // the last ones of their sequences, come first, so that short ones fill the gaps at the
 // end: among up to 64 sequences by their number in the sequence, else each sequence's
 // from its last to its first. false: no such block.
+template <int ROWS>
 __device__ __forceinline__ bool find_block(const Args& a, int blk, int& seq, int& first) {
     const int lane = threadIdx.x & 63;
     if (a.batch <= 64) {
-        const int n = blocks_of(a, lane);
+        const int n = blocks_of<ROWS>(a, lane);
         // blocks numbered k or more: the sum of max(0, n - k); find the k of block blk
         const auto from = [&](int k) { return __builtin_amdgcn_readlane(wave_incl_sum(n > k ? n - k : 0), 63); };
         if (blk >= from(0)) return false;
@@ -208,21 +214,21 @@ __device__ __forceinline__ bool find_block(const Args& a, int blk, int& seq, int
         const int at = blk - from(lo + 1);
         const uint64_t hit = __ballot(n > lo && __popcll(there & ((1ull << lane) - 1)) == at);
         seq = __ffsll((unsigned long long)hit) - 1;
-        first = lo * kRows;
+        first = lo * ROWS;
         return true;
     }
     int total = 0;
     for (int pass = 0; pass < 2; ++pass) {
         int before = 0;
         for (int b0 = 0; b0 < a.batch; b0 += 64) {
-            const int n = blocks_of(a, b0 + lane);
+            const int n = blocks_of<ROWS>(a, b0 + lane);
             const int incl = wave_incl_sum(n);
             if (pass == 1) {
                 const uint64_t hit = __ballot(n > 0 && before + incl - n <= blk && blk < before + incl);
                 if (hit) {
                     const int l = __ffsll((unsigned long long)hit) - 1;
                     seq = b0 + l;
-                    first = (blk - before - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l))) * kRows;
+                    first = (blk - before - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l))) * ROWS;
                     return true;
                 }
             }
@@ -237,11 +243,11 @@ __device__ __forceinline__ bool find_block(const Args& a, int blk, int& seq, int
     return false;
 }
 
-template <int D, int RW, bool BF16>
-__global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a) {
+template <int D, int RW, int ROWS, bool BF16>
+__global__ __launch_bounds__(64 * ROWS / RW, 2) void attn_prompt_kernel(Args a) {
     typedef Shape<RW> Sh;
     typedef typename Sh::acc acc;
-    constexpr int KD = Sh::KD, VE = Sh::VE, kThreads = 64 * kRows / RW;
+    constexpr int KD = Sh::KD, VE = Sh::VE, kThreads = 64 * ROWS / RW;
     constexpr int NS = D / KD;                 // contraction steps of the scores
     constexpr int NT = kPos / RW;              // blocks of positions of the scores
     constexpr int ND = D / RW;                 // column blocks of the output
@@ -253,7 +259,7 @@ __global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int head = blockIdx.x % a.kv_heads;
     int b, first;
-    if (!find_block(a, blockIdx.x / a.kv_heads, b, first)) return;
+    if (!find_block<ROWS>(a, blockIdx.x / a.kv_heads, b, first)) return;
     const int q0 = a.cu_q[b], nq = a.cu_q[b + 1] - q0;
     if (q0 < 0 || (long long)q0 + nq > a.rows_q) return;
     int k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
@@ -275,7 +281,7 @@ __global__ __launch_bounds__(64 * kRows / RW, 2) void attn_prompt_kernel(Args a)
     for (int st = 0; st < NS; ++st) qf[st] = live ? *(const s16x8*)(qp + KD * st) : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
 
     // tiles that some row of the workgroup sees, and those that all see whole
-    const int last_row = first + kRows < rows ? first + kRows - 1 : rows - 1;
+    const int last_row = first + ROWS < rows ? first + ROWS - 1 : rows - 1;
     const int at_first = first / a.group + shift, at_last = last_row / a.group + shift;
     const int t_hi = at_last >= 0 ? (at_last >> 6) + 1 : 0;
     const int t_lo = kv::first_seen(at_first, a.window) >> 6;
@@ -440,8 +446,9 @@ XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int
         (type != XP_BF16 && type != XP_F16) || window < 0 || !(scale > 0.0f && scale < __builtin_inff()))
         return XP_ERR_SHAPE;
     const int group = heads / kv_heads;
-    const int64_t blocks = ((int64_t)rows_q * group + kRows - 1) / kRows + batch;
-    if ((int64_t)rows_q * group > 0x7fffffff - kRows || rows_k > 0x7fffffff - kPos || blocks * kv_heads >= (1 << 23))   // a launch has fewer than 2^32 threads
+    // workgroups of 64 rows, the smaller of the two kinds
+    const int64_t small = ((int64_t)rows_q * group + 63) / 64 + batch, large = ((int64_t)rows_q * group + 127) / 128 + batch;
+    if ((int64_t)rows_q * group > 0x7fffffff - 128 || rows_k > 0x7fffffff - kPos || small * kv_heads >= (1 << 23))   // a launch has fewer than 2^32 threads
         return XP_ERR_SHAPE;
     if (batch == 0 || rows_q == 0) return XP_OK;
     if (!q || !cu_q || !cu_k || !out || (rows_k > 0 && (!k || !v))) return XP_ERR_NULL;
@@ -453,22 +460,26 @@ XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int
         return XP_ERR_SHAPE;
     const Args a{(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)out, q_stride, k_stride, v_stride,
                  out_stride, cu_q, cu_k, rows_q, rows_k, batch, kv_heads, group, window, kv::log2_scale(scale)};
-    const dim3 grid((unsigned)(blocks * kv_heads));
     hipStream_t s = (hipStream_t)stream;
-#define XP_PROMPT_LAUNCH(D_, RW_)                                                                  \
+#define XP_PROMPT_LAUNCH(D_, RW_, ROWS_, BLOCKS_)                                                  \
     do {                                                                                           \
-        const dim3 block(64 * kRows / RW_);                                                        \
+        const dim3 grid((unsigned)(BLOCKS_ * kv_heads)), block(64 * ROWS_ / RW_);                  \
         if (type == XP_BF16)                                                                       \
-            hipLaunchKernelGGL((attn_prompt_kernel<D_, RW_, true>), grid, block, 0, s, a);         \
+            hipLaunchKernelGGL((attn_prompt_kernel<D_, RW_, ROWS_, true>), grid, block, 0, s, a);  \
         else                                                                                       \
-            hipLaunchKernelGGL((attn_prompt_kernel<D_, RW_, false>), grid, block, 0, s, a);        \
+            hipLaunchKernelGGL((attn_prompt_kernel<D_, RW_, ROWS_, false>), grid, block, 0, s, a); \
     } while (0)
-    if (head_dim == 64)
-        XP_PROMPT_LAUNCH(64, 32);
+    const bool few = large * kv_heads <= kFew;
+    if (head_dim == 256)
+        XP_PROMPT_LAUNCH(256, 16, 128, large);
+    else if (head_dim == 128 && few)
+        XP_PROMPT_LAUNCH(128, 16, 64, small);
     else if (head_dim == 128)
-        XP_PROMPT_LAUNCH(128, 32);
+        XP_PROMPT_LAUNCH(128, 32, 128, large);
+    else if (few)
+        XP_PROMPT_LAUNCH(64, 16, 64, small);
     else
-        XP_PROMPT_LAUNCH(256, 16);
+        XP_PROMPT_LAUNCH(64, 32, 128, large);
 #undef XP_PROMPT_LAUNCH
     return launch_status();
 }

@@ -619,6 +619,28 @@ def test_prompt_many_sequences():
     check_prompt(q, k, v, cu, cu, out, 0.125)
 
 
+@pytest.mark.parametrize("dim,ty,window", [(64, "bf16", 0), (64, "f16", 90), (128, "bf16", 70), (128, "f16", 0)])
+def test_prompt_many_workgroups(dim, ty, window):
+    """More workgroups than take the form for few of them: ragged prompts with prefixes, values that are
+    not finite behind and before what rows see."""
+    rng = np.random.default_rng(400 + dim)
+    nq, prefix, kv, group = [150, 129, 0, 64, 1], [0, 70, 5, 0, 100], 64, 2
+    nk = [a + b for a, b in zip(nq, prefix)]
+    cu_q, cu_k = ends(nq), ends(nk)
+    assert ((cu_q[-1] * group + 127) // 128 + len(nq)) * kv > 512
+    q = dev(rng.normal(size=(cu_q[-1] + 2, kv * group, dim)) * 2, DT[ty])
+    k, v = (rng.normal(size=(cu_k[-1], kv, dim)) for _ in "kv")
+    v[100, :, 3], v[130, 5, 7], v[20, 6, 1] = np.nan, np.inf, -np.inf     # first sequence
+    v[cu_k[1] + 190, 9, :], k[cu_k[1] + 180, 10, 2] = np.nan, np.nan      # near the second's end
+    k, v = dev(k, DT[ty]), dev(v, DT[ty])
+    out = torch.full_like(q, 4.0)
+    xp.xp_attn_prompt(q, k, v, dev(cu_q), dev(cu_k), dim ** -0.5, out, window=window)
+    worst = check_prompt(q, k, v, cu_q, cu_k, out, dim ** -0.5, window)
+    assert (out[int(cu_q[-1]):] == 4.0).all()
+    assert torch.isfinite(out[:20].float()).all()
+    print("share of the bound: %.2f" % worst, flush=True)
+
+
 @pytest.mark.parametrize("ty", ["bf16", "f16"])
 def test_prompt_what_a_row_does_not_see(ty):
     """NaN and infinities in later positions, outside the window and in the next sequence stay away."""
