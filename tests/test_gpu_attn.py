@@ -234,6 +234,41 @@ def test_decode_ragged_batches(batch, max_len):
     check_decode(c, table, lens, q, out, 0.125, q_rows=2)
 
 
+@pytest.mark.parametrize("dim,group,q_rows,n,window", [(128, 8, 5, 3000, 0), (64, 4, 9, 4100, 0), (256, 8, 3, 2500, 0),
+                                                       (128, 8, 5, 5000, 2100)])
+def test_decode_many_rows_over_cut_sequences(dim, group, q_rows, n, window):
+    """More than sixteen rows a kv head over contexts cut into pieces, with weights."""
+    rng = np.random.default_rng(n)
+    kv, page = 2, 128
+    cols = -(-n // page)
+    c = filled(rng, kv, dim, page, 2 * cols)
+    table = tables(rng, 2, cols, 2 * cols)
+    lens = np.array([n, 777], dtype=np.int32)
+    q = dev(rng.normal(size=(2 * q_rows, kv * group, dim)) * 2, torch.bfloat16)
+    w = torch.rand(2, kv, cols * page, device="cuda")
+    w0 = w.clone()
+    out = run_decode(c, on_device(c), table, lens, q, dim ** -0.5, window, q_rows, weights=w)
+    check_decode(c, table, lens, q, out, dim ** -0.5, window, q_rows, base=w0, weights=w)
+
+
+@pytest.mark.parametrize("batch,longest", [(40, 300), (64, 17000), (64, 130)])
+def test_decode_many_units(batch, longest):
+    """More units than CUs: whole sequences in order of length, and one that is cut all the same."""
+    rng = np.random.default_rng(batch + longest)
+    kv, dim, page = 8, 64, 64
+    lens = rng.integers(0, 130, batch).astype(np.int32)
+    lens[17], lens[3] = longest, 0
+    cols = -(-longest // page)
+    c = filled(rng, kv, dim, page, 280)
+    table = np.full((batch, cols), -1, dtype=np.int32)
+    for b in range(batch):                                 # pages that are only read may be shared
+        m = -(-int(lens[b]) // page)
+        table[b, :m] = rng.permutation(280)[:m]
+    q = dev(rng.normal(size=(batch, kv, dim)) * 2, torch.float16)
+    out = run_decode(c, on_device(c), table, lens, q, 0.125)
+    check_decode(c, table, lens, q, out, 0.125)
+
+
 def test_windows_as_wide_as_an_int():
     """A window of 2^31 - 1 is none, also where queries lie before the first key."""
     rng = np.random.default_rng(77)
