@@ -483,8 +483,9 @@ static int check_rows(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, 
                       const void* cache) {
     const int st = check_geo(dims, batch, max_pages);
     if (st != XP_OK) return st;
-    if (rows < 0 || rows > 0x7fffffff - 64 || (int64_t)rows * dims->kv_heads >= (1 << 30) || type < XP_BF16 || type > XP_F32)
-        return XP_ERR_SHAPE;
+    if (rows < 0 || rows > 0x7fffffff - 64 || type < XP_BF16 || type > XP_F32) return XP_ERR_SHAPE;
+    // a launch has fewer than 2^32 threads, 256 for 64 rows of a kv head
+    if (((int64_t)rows + kBlockRows - 1) / kBlockRows * dims->kv_heads >= (1 << 24)) return XP_ERR_SHAPE;
     if (rows == 0 || batch == 0) return XP_OK;
     if (!k || !v || !cu || !start || !table || !cache) return XP_ERR_NULL;
     const int64_t width = (int64_t)dims->kv_heads * dims->head_dim, unit = type == XP_F32 ? 4 : 8;

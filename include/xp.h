@@ -381,9 +381,9 @@ int xp_kv_append(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32
 
 /* The reverse, for the same row map: the cached values as `type` (any xp_type; all
  * three hold them exactly). Rows whose position the cache does not have are 0; rows
- * from cu_rows[batch] on are left as they were. rows * kv_heads is below 2^30 for both
- * calls. A prompt's next piece reads its
- * prefix back with it for xp_attn_prompt. */
+ * from cu_rows[batch] on are left as they were. For both calls kv_heads times the blocks
+ * of 64 rows, a part of one counted whole, is below 2^24. A prompt's next piece reads
+ * its prefix back with it for xp_attn_prompt. */
 int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, int32_t type,
                const int32_t* cu_rows, const int32_t* start, const int32_t* table, const uint8_t* cache, void* k,
                int64_t k_stride, void* v, int64_t v_stride, void* stream);

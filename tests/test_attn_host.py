@@ -72,6 +72,13 @@ def test_row_calls_refuse(name):
     assert call(batch=0, **none) == xp.XP_OK
 
 
+@pytest.mark.parametrize("name", ["xp_kv_append", "xp_kv_read"])
+def test_row_calls_refuse_launches_of_2_32_threads(name):
+    """64 rows of a kv head are a workgroup of 256: 2^14 such blocks, the last one short, times 1,024 heads are one too many."""
+    for rows in ((1 << 20) - 1, (1 << 20) - 63):
+        assert _rows_call(name, g=kd(kv=1024), rows=rows, ks=65536, vs=65536) == xp.XP_ERR_SHAPE, rows
+
+
 def _decode(**kw):
     a = dict(g=kd(), heads=4, q_rows=1, batch=1, cols=1, max_len=64, ty=BF16, q=P, qs=256, scale=1.0, window=0, cache=P,
              table=P, lens=P, out=P, os=256, weights=None, ws=0, work=P, bytes=1 << 30)
