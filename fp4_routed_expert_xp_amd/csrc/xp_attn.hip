@@ -16,7 +16,10 @@
 // Precision: codes times scales are exact in fp16 (six significant bits). q in
 // bf16 is scaled by a power of two to fp16, row by row, which is exact for every
 // value within 2^28 of its row's largest. Scores, maxima, sums and outputs are
-// fp32. Exponentials round once to fp16 (2^-11), held as 2^15 p: what falls below
+// fp32. The maximum is kept as the score it is, and the factor to log2 units multiplies
+// differences only: the largest exponential is then 2^15 exactly for scores of any size
+// (a maximum in log2 units has steps of 2 from 2^24 on, which fp16 does not survive).
+// Exponentials round once to fp16 (2^-11), held as 2^15 p: what falls below
 // fp16's normal numbers is then within 2^-40 of the row's largest.
 //
 // Bound by the cache's bytes where contexts are long: 64 ragged sequences to 8,192
@@ -50,7 +53,7 @@ struct Args {
     void* out;
     long long out_stride;
     float* part;          // partial outputs of cut sequences' pieces, unscaled
-    float* part_ml;       // their maxima and sums
+    float* part_ml;       // their maxima (of the scores as they are formed), sums and the rows' factors
     float* lse;           // per row: the maximum in log2 units and the sum's logarithm, for the weights
     float* weights;
     long long w_stride;
@@ -569,21 +572,21 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
             float mx = s[mt][0][0];
 #pragma unroll
             for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[mt][e >> 2][e & 3]);
-            mx = max_over_q(mx) * factor[mt];
+            mx = max_over_q(mx);
             if (__ballot(mx > m[mt])) {
                 const float nm = fmaxf(mx, m[mt]);
                 const float safe = nm == -__builtin_inff() ? 0.0f : nm;
-                const float alpha = __builtin_amdgcn_exp2f(m[mt] - safe);
+                const float alpha = __builtin_amdgcn_exp2f((m[mt] - safe) * factor[mt]);
                 m[mt] = nm;
                 l[mt] *= alpha;
 #pragma unroll
                 for (int h = 0; h < NH; ++h) o[mt][h] *= alpha;
             }
-            const float base = kLift - (m[mt] == -__builtin_inff() ? 0.0f : m[mt]);
+            const float top = m[mt] == -__builtin_inff() ? 0.0f : m[mt];
             float add = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][e >> 2][e & 3], factor[mt], base));
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][e >> 2][e & 3] - top, factor[mt], kLift));
                 add += x;
                 p[mt][e >> 3][e & 7] = (_Float16)x;
             }
@@ -668,6 +671,7 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
     const long long slot = pc.slot + (long long)pc.index * (a.g.kv_heads * a.row_blocks);
     for (int col_block = wave; col_block < MT * NH; col_block += waves) {
         const int mt = MT == 1 ? 0 : col_block / NH, h = col_block - mt * NH;
+        const float fr = mt == 0 ? factor[0] : factor[MT - 1];
         float jm = -__builtin_inff(), jl = 0.0f;
         for (int w = 0; w < waves; ++w)
             jm = fmaxf(jm, ((const float*)(lds + w * join_bytes<D, MT>() + MT * NH * 1024))[mt * 32 + c]);
@@ -676,16 +680,17 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
         for (int w = 0; w < waves; ++w) {
             const uint8_t* from = lds + w * join_bytes<D, MT>();
             const float* ml = (const float*)(from + MT * NH * 1024) + mt * 32 + c;
-            const float f = __builtin_amdgcn_exp2f(ml[0] - safe);
+            const float f = __builtin_amdgcn_exp2f((ml[0] - safe) * fr);
             jl = __builtin_fmaf(ml[16], f, jl);
             acc += ((const f32x4*)from)[col_block * 64 + lane] * f;
         }
         if (pc.pieces > 1) {
             ((f32x4*)a.part)[(slot * (MT * NH) + col_block) * 64 + lane] = acc;
-            float* pm = a.part_ml + slot * (MT * 32);
+            float* pm = a.part_ml + slot * (MT * 48) + mt * 48 + c;
             if (h == 0 && q == 0) {
-                pm[mt * 32 + c] = jm;
-                pm[mt * 32 + 16 + c] = jl;
+                pm[0] = jm;
+                pm[16] = jl;
+                pm[32] = fr;
             }
             continue;
         }
@@ -696,7 +701,7 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
         const float inv = jl == 0.0f ? 0.0f : 1.0f / jl;   // nothing seen: zeros
         *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(acc * inv);
         if (a.lse && h == 0 && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
-            jl == 0.0f ? __builtin_inff() : (jm - kLift) + __builtin_amdgcn_logf(jl);
+            jl == 0.0f ? __builtin_inff() : __builtin_fmaf(jm, fr, __builtin_amdgcn_logf(jl) - kLift);
     }
 }
 
@@ -718,7 +723,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
     const int b = pc.b, rb = pc.unit / a.g.kv_heads, head = pc.unit - rb * a.g.kv_heads, n = pc.pieces;
     const long long step = a.g.kv_heads * a.row_blocks;    // slots from one piece of a unit to its next
     const f32x4* po = (const f32x4*)a.part + (long long)pc.slot * (MT * NH * 64) + blockIdx.x * 64 + lane;
-    const float* pm = a.part_ml + (long long)pc.slot * (MT * 32) + mt * 32 + c;
+    const float* pm = a.part_ml + (long long)pc.slot * (MT * 48) + mt * 48 + c;
+    const float fr = pm[32];                               // the row's factor, the same with every piece
     float m = -__builtin_inff(), l = 0.0f;
     f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
     constexpr int U = 8;
@@ -729,14 +735,14 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * waves < n ? s0 + u * waves : s0;
             v[u] = po[s * step * (MT * NH * 64)];
-            vm[u] = pm[s * step * (MT * 32)];
-            vl[u] = pm[s * step * (MT * 32) + 16];
+            vm[u] = pm[s * step * (MT * 48)];
+            vl[u] = pm[s * step * (MT * 48) + 16];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s0 + u * waves >= n) break;
             const float nm = fmaxf(m, vm[u]), safe = nm == -__builtin_inff() ? 0.0f : nm;
-            const float fa = __builtin_amdgcn_exp2f(m - safe), fb = __builtin_amdgcn_exp2f(vm[u] - safe);
+            const float fa = __builtin_amdgcn_exp2f((m - safe) * fr), fb = __builtin_amdgcn_exp2f((vm[u] - safe) * fr);
             m = nm;
             l = l * fa + vl[u] * fb;
             o = o * fa + v[u] * fb;
@@ -750,7 +756,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
     if (wave > 0 || r >= a.q_rows * a.group) return;
     for (int w = 1; w < waves; ++w) {
         const float om = sm[w][lane], nm = fmaxf(m, om), safe = nm == -__builtin_inff() ? 0.0f : nm;
-        const float fa = __builtin_amdgcn_exp2f(m - safe), fb = __builtin_amdgcn_exp2f(om - safe);
+        const float fa = __builtin_amdgcn_exp2f((m - safe) * fr), fb = __builtin_amdgcn_exp2f((om - safe) * fr);
         m = nm;
         l = l * fa + sl[w][lane] * fb;
         o = o * fa + so[w][lane] * fb;
@@ -760,7 +766,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
     uint16_t* y = (uint16_t*)a.out + ((long long)b * a.q_rows + tok) * a.out_stride + (long long)hd * D;
     *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(o * inv);
     if (a.lse && h == 0 && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
-        l == 0.0f ? __builtin_inff() : (m - kLift) + __builtin_amdgcn_logf(l);
+        l == 0.0f ? __builtin_inff() : __builtin_fmaf(m, fr, __builtin_amdgcn_logf(l) - kLift);
 }
 
 // weights[pos] += the probabilities of all rows of the kv head at pos, from each
@@ -884,7 +890,7 @@ static Launch plan_of(const xp_kv_dims* d, int heads, int q_rows, int batch, int
     const size_t parts = 2 * (size_t)p.share;
     p.part = 0;
     p.ml = parts * 16 * p.mt * d->head_dim * sizeof(float);
-    p.lse = p.ml + align256(parts * 32 * p.mt * sizeof(float));
+    p.lse = p.ml + align256(parts * 48 * p.mt * sizeof(float));
     p.total = p.lse + align256((size_t)batch * heads * q_rows * sizeof(float));
     return p;
 }

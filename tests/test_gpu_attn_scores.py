@@ -1,0 +1,68 @@
+"""GPU: attention where scores are far from the ordinary: finite queries and keys whose scores reach
+far beyond fp16's range in log2 units."""
+import numpy as np
+import pytest
+import torch
+
+import attn_ref as ref
+from test_gpu_attn import DT, dev, filled, on_device, run_decode, tables
+
+pytestmark = pytest.mark.gpu
+
+
+def loud_cache(rng, kv, dim, page, pages):
+    """K holds +-48 everywhere (code 7 or 15 times the scale 8), V values of ordinary size."""
+    c = filled(rng, kv, dim, page, pages)
+    n = c.ng * 1024
+    c.b[..., :n] = 0x77 | (rng.integers(0, 2, c.b.shape[:3] + (n,)) * 0x80 + rng.integers(0, 2, c.b.shape[:3] + (n,)) * 0x08)
+    c.b[..., n:n + c.ng * 64] = 0x50                       # E4M3 8.0
+    return c
+
+
+@pytest.mark.parametrize("ty,mag", [("f16", 32000.0), ("f16", 2000.0), ("bf16", 1e6), ("bf16", 1e30)])
+@pytest.mark.parametrize("dim,group,q_rows,n", [(128, 4, 1, 300), (128, 8, 5, 300), (64, 8, 2, 5000), (256, 3, 1, 900)])
+def test_decode_large_finite_scores(dim, group, q_rows, n, ty, mag):
+    """Each row's query points along one key that it sees (of random signs, so that no other comes near):
+    its weight is 1 to within 2^-1000 of it, every other's 0, and the output is that position's v, which the
+    output type holds exactly. Scores reach mag * 48 * sqrt(dim) (2^19 .. 2^110 in log2 units)."""
+    rng = np.random.default_rng(dim + n + int(np.log2(mag)))
+    kv, page, batch = 2, 128, 3
+    lens = np.array([n, 257, 70], dtype=np.int32)
+    cols = -(-n // page)
+    c = loud_cache(rng, kv, dim, page, batch * cols)
+    table = tables(rng, batch, cols, batch * cols)
+    q = np.zeros((batch * q_rows, kv * group, dim))
+    want = np.zeros_like(q)
+    for b in range(batch):
+        for h in range(kv):
+            k, _ = c.rows(table[b], h, int(lens[b]), "k")
+            v, _ = c.rows(table[b], h, int(lens[b]), "v")
+            for i in range(q_rows):
+                for g in range(group):
+                    j = int(rng.integers(0, lens[b] - q_rows + i + 1))
+                    q[b * q_rows + i, h * group + g] = np.sign(k[j]) * mag * rng.uniform(1.0, 2.0)
+                    want[b * q_rows + i, h * group + g] = v[j]
+    out = run_decode(c, on_device(c), table, lens, dev(q, DT[ty]), dim ** -0.5, q_rows=q_rows)
+    np.testing.assert_array_equal(out.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16"])
+def test_decode_large_equal_scores(ty):
+    """Two equal keys at the top of huge scores weigh a half each, wherever they lie (one wave, several, several
+    pieces); v holds whole quarters there, so their mean is exact in both types."""
+    rng = np.random.default_rng(9)
+    kv, dim, page, n = 1, 64, 64, 6000
+    cols = -(-n // page)
+    c = loud_cache(rng, kv, dim, page, cols)
+    table = tables(rng, 1, cols, cols)
+    one = (np.full(dim, 6, dtype=np.uint8), np.full(2, 0x38, dtype=np.uint8))        # 4 in every column
+    two = (np.full(dim, 12, dtype=np.uint8), np.full(2, 0x38, dtype=np.uint8))       # -2
+    for at in ((5, 40), (6, 64 * 7 + 3), (100, 5990)):
+        a, b = ((int(table[0, p // page]), 0, p % page) for p in at)
+        c.put(*b, "k", *c.get(*a, "k"))
+        c.put(*a, "v", *one)
+        c.put(*b, "v", *two)
+        k, _ = c.rows(table[0], 0, n, "k")
+        q = dev(np.stack([np.sign(k[at[0]]) * m for m in rng.uniform(3e4, 6.5e4, 8)])[None], DT[ty])
+        out = run_decode(c, on_device(c), table, np.array([n], dtype=np.int32), q, 0.125)
+        assert (out == 1.0).all(), at
