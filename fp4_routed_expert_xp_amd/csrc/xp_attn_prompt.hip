@@ -44,6 +44,7 @@ constexpr int kPos = 64;     // positions of a tile
 // 32/8 (512) 58 and 60; eight packed prompts to 1,000 (1,190) 83 and 61.
 constexpr int kFew = 512;
 constexpr float kLag = 8.0f; // of the running maximum, in powers of two
+constexpr float kNear = 256.0f;   // maxima in log2 units up to which a product with the factor is used
 
 struct Args {
     const uint16_t* q;
@@ -55,6 +56,7 @@ struct Args {
     const int32_t* cu_k;
     int rows_q, rows_k, batch, kv_heads, group, window;
     float scale_log2;
+    float lag;            // kLag in units of the scores
 };
 
 // What a wave of RW rows has of its products: RW x RW results, VE a lane, over KD of
@@ -293,6 +295,7 @@ __global__ __launch_bounds__(64 * ROWS / RW, 2) void attn_prompt_kernel(Args a) 
 #pragma unroll
         for (int r = 0; r < VE; ++r) o[d][r] = 0.0f;
     float mx = -__builtin_inff(), sum = 0.0f;
+    uint64_t far = 0;                          // lanes whose maximum is too large for that
 
     const uint16_t* kp = a.k + (long long)k0 * a.k_stride + (long long)head * D;
     const uint16_t* vp = a.v + (long long)k0 * a.v_stride + (long long)head * D;
@@ -368,18 +371,26 @@ __global__ __launch_bounds__(64 * ROWS / RW, 2) void attn_prompt_kernel(Args a) 
         float top = s[0][0];
 #pragma unroll
         for (int e = 1; e < NT * VE; ++e) top = fmaxf(top, s[e / VE][e % VE]);
-        top = over_q<RW, false>(top) * a.scale_log2;
+        top = over_q<RW, false>(top);
         // Exponentials are taken from a maximum that lags behind by up to kLag: they stay below
-        // 2^kLag, and what was summed needs no factor but in a row's first tiles.
-        if (__ballot(top > mx + kLag)) {
-            const float nm = fmaxf(top, mx);
-            const float alpha = __builtin_amdgcn_exp2f(mx - (nm == -__builtin_inff() ? 0.0f : nm));
+        // 2^kLag, and what was summed needs no factor but in a row's first tiles. mx is the score
+        // as it is. Up to kNear in log2 units its product with the factor, rounded, is within
+        // 2^-17 of the maximum, far below the exponentials' own rounding, and one fma does;
+        // beyond that the factor multiplies differences only, which is right at any size, and
+        // nothing lags.
+        if (__builtin_expect((__ballot(top > mx + a.lag) | far) != 0, 0)) {
+            const float nm = fmaxf(top, mx), from = nm == -__builtin_inff() ? 0.0f : nm;
+            const float alpha = __builtin_amdgcn_exp2f((mx - from) * a.scale_log2);
             mx = nm;
+            far = __ballot(!(__builtin_fabsf(from * a.scale_log2) <= kNear));
+            if (far)
+#pragma unroll
+                for (int e = 0; e < NT * VE; ++e) s[e / VE][e % VE] -= from;
             sum *= alpha;
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[d] *= alpha;
         }
-        const float base = mx == -__builtin_inff() ? 0.0f : -mx;
+        const float base = far || mx == -__builtin_inff() ? 0.0f : -mx * a.scale_log2;
         // The sum is of the rounded exponentials, two at a time: what rounding adds to a weight
         // that stands out it adds to the sum as well (a maximum that lags is not 1 exactly).
         s16x8 p[NT * VE / 8];
@@ -458,8 +469,10 @@ XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int
     if (q_stride < qw || out_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
         out_stride % 4 || !kv::aligned_to(q, 16) || !kv::aligned_to(k, 16) || !kv::aligned_to(v, 16) || !kv::aligned_to(out, 8) || !kv::aligned_to(cu_q, 4) || !kv::aligned_to(cu_k, 4))
         return XP_ERR_SHAPE;
+    const float f = kv::log2_scale(scale);
     const Args a{(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)out, q_stride, k_stride, v_stride,
-                 out_stride, cu_q, cu_k, rows_q, rows_k, batch, kv_heads, group, window, kv::log2_scale(scale)};
+                 out_stride, cu_q, cu_k, rows_q, rows_k, batch, kv_heads, group, window, f,
+                 kLag / f < 0x1p127f ? kLag / f : 0x1p127f};   // finite: the maximum may be -infinity
     hipStream_t s = (hipStream_t)stream;
 #define XP_PROMPT_LAUNCH(D_, RW_, ROWS_, BLOCKS_)                                                  \
     do {                                                                                           \

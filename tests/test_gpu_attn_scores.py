@@ -4,8 +4,10 @@ import numpy as np
 import pytest
 import torch
 
+from fp4_routed_expert_xp_amd import xp
+
 import attn_ref as ref
-from test_gpu_attn import DT, dev, filled, on_device, run_decode, tables
+from test_gpu_attn import DT, dev, ends, filled, on_device, run_decode, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +68,50 @@ def test_decode_large_equal_scores(ty):
         q = dev(np.stack([np.sign(k[at[0]]) * m for m in rng.uniform(3e4, 6.5e4, 8)])[None], DT[ty])
         out = run_decode(c, on_device(c), table, np.array([n], dtype=np.int32), q, 0.125)
         assert (out == 1.0).all(), at
+
+
+@pytest.mark.parametrize("ty,mag,key", [("f16", 32000.0, 1000.0), ("f16", 32000.0, 60000.0), ("bf16", 1e6, 1e6),
+                                        ("bf16", 1e15, 1e18), ("f16", 100.0, 50.0)])
+@pytest.mark.parametrize("kv,group,dim,nq,prefix", [(2, 4, 128, [300, 70], [0, 40]), (2, 2, 64, [200], [0]),
+                                                    (1, 3, 256, [150], [130]), (64, 2, 64, [200, 130], [0, 70]),
+                                                    (64, 2, 128, [200, 130], [0, 70])])
+def test_prompt_large_finite_scores(kv, group, dim, nq, prefix, ty, mag, key):
+    """As test_decode_large_finite_scores: scores reach mag * key * sqrt(dim) (2^16 .. 2^113 in log2 units), and
+    each row's output is the v of the one key along which its query points. All forms of the kernel."""
+    rng = np.random.default_rng(dim + kv + int(np.log2(mag * key)))
+    nk = [a + b for a, b in zip(nq, prefix)]
+    cu_q, cu_k = ends(nq), ends(nk)
+    k = rng.choice([-key, key], size=(cu_k[-1], kv, dim))
+    v = torch.from_numpy(rng.normal(size=k.shape)).to(DT[ty])
+    q, want = np.zeros((cu_q[-1], kv * group, dim)), torch.zeros(int(cu_q[-1]), kv * group, dim, dtype=DT[ty])
+    for b in range(len(nq)):
+        for i in range(nq[b]):
+            j = cu_k[b] + rng.integers(0, prefix[b] + i + 1, kv * group)
+            heads = np.arange(kv * group) // group
+            q[cu_q[b] + i] = np.sign(k[j, heads]) * mag * rng.uniform(1.0, 2.0, (kv * group, 1))
+            want[cu_q[b] + i] = v[torch.from_numpy(j), torch.from_numpy(heads)]
+    q, k, v = dev(q, DT[ty]), dev(k, DT[ty]), v.cuda()
+    out = torch.empty_like(q)
+    xp.xp_attn_prompt(q, k, v, dev(cu_q), dev(cu_k), dim ** -0.5, out)
+    np.testing.assert_array_equal(out.cpu().double().numpy(), want.double().numpy())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("ty", ["bf16", "f16"])
+def test_prompt_large_equal_scores(dim, ty):
+    """Two equal keys at the top of huge scores, in one tile and in different ones, weigh a half each."""
+    rng = np.random.default_rng(dim)
+    n = 400
+    k = rng.choice([-1000.0, 1000.0], size=(n, 1, dim))
+    v = rng.normal(size=(n, 1, dim))
+    pairs = [(0, 1), (3, 60), (10, 200), (130, 390)]
+    for a, b in pairs:
+        k[b], v[a], v[b] = k[a], 4.0, -2.0
+    q = rng.choice([-1.0, 1.0], size=(n, 4, dim))
+    for h, (a, b) in enumerate(pairs):
+        q[b:, h] = np.sign(k[a, 0]) * rng.uniform(3e4, 6.5e4, (n - b, 1))
+    out = torch.empty(n, 4, dim, dtype=DT[ty], device="cuda")
+    cu = dev(ends([n]))
+    xp.xp_attn_prompt(dev(q, DT[ty]), dev(k, DT[ty]), dev(v, DT[ty]), cu, cu, dim ** -0.5, out)
+    for h, (a, b) in enumerate(pairs):
+        assert (out[b:, h] == 1.0).all(), h
