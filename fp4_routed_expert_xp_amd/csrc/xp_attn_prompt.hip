@@ -22,7 +22,8 @@
 // bank conflicts.
 //
 // Scores, maxima, sums and outputs are fp32; exponentials round once to the type of
-// v (the product's operand), the result once to the output type.
+// v (the product's operand; in fp16 as 2^13 times the weight, so that a long tail of
+// small weights is not lost), the result once to the output type.
 #include "xp_kv_dev.h"
 
 namespace xp {
@@ -43,7 +44,12 @@ constexpr int kPos = 64;     // positions of a tile
 // workgroups) take 48 us so and 58 us in 128 rows, 1,000 of 32/8 28 and 33; 2,000 of
 // 32/8 (512) 58 and 60; eight packed prompts to 1,000 (1,190) 83 and 61.
 constexpr int kFew = 512;
-constexpr float kLag = 8.0f; // of the running maximum, in powers of two
+// In powers of two: by how much the running maximum may lag behind, and what exponentials are
+// held as times the weight. fp16 has the range for both only together (15), so it lags less:
+// weights down to 2^-27 of the largest then keep all their bits, and what is below is within
+// 2^-38 of it. bf16 has fp32's range.
+constexpr float lag_of(bool bf16) { return bf16 ? 8.0f : 2.0f; }
+constexpr float lift_of(bool bf16) { return bf16 ? 0.0f : 13.0f; }
 constexpr float kNear = 256.0f;   // maxima in log2 units up to which a product with the factor is used
 
 struct Args {
@@ -56,7 +62,7 @@ struct Args {
     const int32_t* cu_k;
     int rows_q, rows_k, batch, kv_heads, group, window;
     float scale_log2;
-    float lag;            // kLag in units of the scores
+    float lag;            // lag_of in units of the scores
 };
 
 // What a wave of RW rows has of its products: RW x RW results, VE a lane, over KD of
@@ -255,6 +261,7 @@ __global__ __launch_bounds__(64 * ROWS / RW, 2) void attn_prompt_kernel(Args a) 
     constexpr int ND = D / RW;                 // column blocks of the output
     constexpr int NL = kPos * D / 8 / kThreads;   // 16-byte chunks a thread stages of each of k and v
     constexpr int kTile = kPos * D * 2;        // bytes of a tile of k, or of v
+    constexpr float kLift = lift_of(BF16);
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * kTile];
 
     const int tid = threadIdx.x, lane = tid & 63, m = lane % RW, q = lane / RW;
@@ -372,12 +379,11 @@ __global__ __launch_bounds__(64 * ROWS / RW, 2) void attn_prompt_kernel(Args a) 
 #pragma unroll
         for (int e = 1; e < NT * VE; ++e) top = fmaxf(top, s[e / VE][e % VE]);
         top = over_q<RW, false>(top);
-        // Exponentials are taken from a maximum that lags behind by up to kLag: they stay below
-        // 2^kLag, and what was summed needs no factor but in a row's first tiles. mx is the score
-        // as it is. Up to kNear in log2 units its product with the factor, rounded, is within
-        // 2^-17 of the maximum, far below the exponentials' own rounding, and one fma does;
-        // beyond that the factor multiplies differences only, which is right at any size, and
-        // nothing lags.
+        // Exponentials are taken from a maximum that lags behind, so what was summed needs no
+        // factor but in a row's first tiles. mx is the score as it is. Up to kNear in log2 units
+        // its product with the factor, rounded, is within 2^-17 of the maximum, far below the
+        // exponentials' own rounding, and one fma does; beyond that the factor multiplies
+        // differences only, which is right at any size, and nothing lags.
         if (__builtin_expect((__ballot(top > mx + a.lag) | far) != 0, 0)) {
             const float nm = fmaxf(top, mx), from = nm == -__builtin_inff() ? 0.0f : nm;
             const float alpha = __builtin_amdgcn_exp2f((mx - from) * a.scale_log2);
@@ -390,7 +396,7 @@ __global__ __launch_bounds__(64 * ROWS / RW, 2) void attn_prompt_kernel(Args a) 
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[d] *= alpha;
         }
-        const float base = far || mx == -__builtin_inff() ? 0.0f : -mx * a.scale_log2;
+        const float base = far || mx == -__builtin_inff() ? kLift : __builtin_fmaf(-mx, a.scale_log2, kLift);
         // The sum is of the rounded exponentials, two at a time: what rounding adds to a weight
         // that stands out it adds to the sum as well (a maximum that lags is not 1 exactly).
         s16x8 p[NT * VE / 8];
@@ -470,9 +476,10 @@ XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int
         out_stride % 4 || !kv::aligned_to(q, 16) || !kv::aligned_to(k, 16) || !kv::aligned_to(v, 16) || !kv::aligned_to(out, 8) || !kv::aligned_to(cu_q, 4) || !kv::aligned_to(cu_k, 4))
         return XP_ERR_SHAPE;
     const float f = kv::log2_scale(scale);
+    const float lag = lag_of(type == XP_BF16) / f;
     const Args a{(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)out, q_stride, k_stride, v_stride,
                  out_stride, cu_q, cu_k, rows_q, rows_k, batch, kv_heads, group, window, f,
-                 kLag / f < 0x1p127f ? kLag / f : 0x1p127f};   // finite: the maximum may be -infinity
+                 lag < 0x1p127f ? lag : 0x1p127f};   // finite: the maximum may be -infinity
     hipStream_t s = (hipStream_t)stream;
 #define XP_PROMPT_LAUNCH(D_, RW_, ROWS_, BLOCKS_)                                                  \
     do {                                                                                           \

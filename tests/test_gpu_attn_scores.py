@@ -115,3 +115,35 @@ def test_prompt_large_equal_scores(dim, ty):
     xp.xp_attn_prompt(dev(q, DT[ty]), dev(k, DT[ty]), dev(v, DT[ty]), cu, cu, dim ** -0.5, out)
     for h, (a, b) in enumerate(pairs):
         assert (out[b:, h] == 1.0).all(), h
+
+
+@pytest.mark.parametrize("nats,spread", [(16.3, 0.0), (17.5, 0.0), (17.5, 3.0)])
+@pytest.mark.parametrize("kv,group,dim,n", [(1, 2, 64, 8192), (1, 2, 128, 8192), (1, 1, 256, 4096), (64, 2, 64, 2048),
+                                            (64, 2, 128, 2048)])
+def test_prompt_f16_long_tail_of_small_weights(kv, group, dim, n, nats, spread):
+    """One key that stands out, with a value of 0, and many that weigh e^-16 to e^-19 of it each: the output is
+    what these add up to.
+
+    Scores are one product each, exact in fp32. The bound, relative to the output (all terms are positive): half a
+    step of the output, a rounding of each weight in the products and in the sum, 2^-11 each; fp32 sums of n terms
+    and the exponential, n 2^-24 + 2^-19; weights below fp16's normal numbers, held as 2^13 times p or more,
+    are off by 2^-38 in the products and in the sum, against their mean."""
+    rng = np.random.default_rng(n + kv)
+    rows = 130
+    k = np.zeros((n, kv, dim))
+    k[1:, :, 0] = -nats + spread * (rng.random((n - 1, kv)) - 0.5)
+    v = rng.uniform(8.0, 24.0, size=(n, kv, dim))
+    v[0] = 0.0
+    q = np.zeros((rows, kv * group, dim))
+    q[:, :, 0] = 1.0
+    q, k, v = (dev(x, torch.float16) for x in (q, k, v))
+    out = torch.empty_like(q)
+    xp.xp_attn_prompt(q, k, v, dev(ends([rows])), dev(ends([n])), 1.0, out)
+    e = torch.exp(k[:, :, 0].double())                                  # [n][kv]
+    num, den = torch.cumsum(e[:, :, None] * v.double(), 0), torch.cumsum(e, 0)
+    want = (num / den[:, :, None])[n - rows:].repeat_interleave(group, 1)
+    assert float(want.min()) > 2.0 ** -13
+    rel = 3 * 2.0 ** -11 + n * 2.0 ** -24 + 2.0 ** -19 + 2 * 2.0 ** -38 / float(e[1:].mean())
+    worst = float(((out.double() - want).abs() / want).max())
+    print("relative error %.2e of %.2e" % (worst, rel), flush=True)
+    assert worst <= rel
