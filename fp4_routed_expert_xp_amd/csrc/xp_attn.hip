@@ -54,7 +54,7 @@ struct Args {
     long long out_stride;
     float* part;          // partial outputs of cut sequences' pieces, unscaled
     float* part_ml;       // their maxima (of the scores as they are formed), sums and the rows' factors
-    float* lse;           // per row: the maximum in log2 units and the sum's logarithm, for the weights
+    float2* stats;        // per row, for the weights: the maximum of its scores and 1 / sum
     float* weights;
     long long w_stride;
     int heads, group, q_rows, row_blocks, window;
@@ -382,6 +382,13 @@ __device__ __forceinline__ bool find_piece(const Args& a, int i, Piece& p) {
     return false;
 }
 
+// A row's statistics for the weights kernel, which forms 2^((s - maximum) factor) times the
+// second: kept apart, for one number in log2 units would round the sum's logarithm to the last
+// place of the maximum. A row that sees nothing weighs nothing (its scores less infinity).
+__device__ __forceinline__ float2 stats_of(float m, float l) {
+    return l == 0.0f ? float2{__builtin_inff(), 0.0f} : float2{m, __builtin_amdgcn_ldexpf(1.0f / l, (int)kLift)};
+}
+
 // Four outputs to 16 bits, nearest even.
 template <bool BF16>
 __device__ __forceinline__ uint2 to16(f32x4 v) {
@@ -700,8 +707,7 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
         uint16_t* y = (uint16_t*)a.out + ((long long)b * a.q_rows + tok) * a.out_stride + (long long)hd * D;
         const float inv = jl == 0.0f ? 0.0f : 1.0f / jl;   // nothing seen: zeros
         *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(acc * inv);
-        if (a.lse && h == 0 && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
-            jl == 0.0f ? __builtin_inff() : __builtin_fmaf(jm, fr, __builtin_amdgcn_logf(jl) - kLift);
+        if (a.stats && h == 0 && q == 0) a.stats[((long long)b * a.heads + head * a.group) * a.q_rows + r] = stats_of(jm, jl);
     }
 }
 
@@ -765,12 +771,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
     const int tok = r / a.group, hd = head * a.group + r - tok * a.group;
     uint16_t* y = (uint16_t*)a.out + ((long long)b * a.q_rows + tok) * a.out_stride + (long long)hd * D;
     *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(o * inv);
-    if (a.lse && h == 0 && q == 0) a.lse[((long long)b * a.heads + head * a.group) * a.q_rows + r] =
-        l == 0.0f ? __builtin_inff() : __builtin_fmaf(m, fr, __builtin_amdgcn_logf(l) - kLift);
+    if (a.stats && h == 0 && q == 0) a.stats[((long long)b * a.heads + head * a.group) * a.q_rows + r] = stats_of(m, l);
 }
 
 // weights[pos] += the probabilities of all rows of the kv head at pos, from each
-// row's logarithm of the sum. Scores are formed with the rows first (S = Q K^T), so
+// row's maximum and sum. Scores are formed with the rows first (S = Q K^T), so
 // a lane adds four rows of one position by itself and two swaps add the rest; one
 // wave owns a tile, so no atomics. K is read a second time: half the cache's bytes,
 // against writing and reading every row's scores (as much for eight rows a head). 18 us
@@ -786,12 +791,13 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
     const int32_t* tr = a.table + (long long)b * a.g.max_pages;
     const int rows = a.q_rows * a.group;
     const int t_lo = span_of(a, len, 0).lo >> 6, t_hi = (len + 63) >> 6;
-    const float* lse = a.lse + ((long long)b * a.heads + head * a.group) * a.q_rows;
+    const float2* stats = a.stats + ((long long)b * a.heads + head * a.group) * a.q_rows;
     float* weights = a.weights + ((long long)b * a.g.kv_heads + head) * a.w_stride;
     const int first = t_lo + blockIdx.x * 4 + wave, step = gridDim.x * 4;
     for (int rb = 0; rb * 16 < rows && first < t_hi; ++rb) {
         h16x8 qf[1][NW];
-        float factor[1], f[4], base[4];
+        float factor[1], f[4];
+        float2 st[4];
         Span sp[4];
         KTile<D> k;
         long long at = kv::tile_at(a.g, tr, head, first * 64);
@@ -804,7 +810,7 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
         for (int i = 0; i < 4; ++i) {
             const int r = rb * 16 + 4 * q + i;
             f[i] = __shfl(factor[0], 4 * q + i);           // held by the lane whose c is the row
-            base[i] = r < rows ? -lse[r] : -__builtin_inff();
+            st[i] = r < rows ? stats[r] : float2{__builtin_inff(), 0.0f};
             sp[i] = span_of(a, len, r);
             if (r >= rows) continue;                       // rows that are not there weigh nothing
             all_lo = sp[i].lo > all_lo ? sp[i].lo : all_lo;
@@ -834,8 +840,8 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
 #pragma unroll
                 for (int bl = 0; bl < 4; ++bl) {
                     const int pos = tile * 64 + 16 * bl + c;
-                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[bl][i], f[i], base[i]));
-                    w[bl] += whole || (pos >= sp[i].lo && pos < sp[i].hi) ? e : 0.0f;
+                    const float e = __builtin_amdgcn_exp2f((s[bl][i] - st[i].x) * f[i]);
+                    w[bl] = whole || (pos >= sp[i].lo && pos < sp[i].hi) ? __builtin_fmaf(e, st[i].y, w[bl]) : w[bl];
                 }
             float mine = 0.0f;
 #pragma unroll
@@ -858,7 +864,7 @@ constexpr int kLongTiles = 256;
 struct Launch {
     int mt, row_blocks, waves, share, chunk, join_waves;
     long long units;
-    size_t part, ml, lse, total;
+    size_t part, ml, stats, total;
 };
 // What a call with these arguments launches and keeps in its workspace (with a window
 // no more than without: it only shortens what is seen).
@@ -890,8 +896,8 @@ static Launch plan_of(const xp_kv_dims* d, int heads, int q_rows, int batch, int
     const size_t parts = 2 * (size_t)p.share;
     p.part = 0;
     p.ml = parts * 16 * p.mt * d->head_dim * sizeof(float);
-    p.lse = p.ml + align256(parts * 48 * p.mt * sizeof(float));
-    p.total = p.lse + align256((size_t)batch * heads * q_rows * sizeof(float));
+    p.stats = p.ml + align256(parts * 48 * p.mt * sizeof(float));
+    p.total = p.stats + align256((size_t)batch * heads * q_rows * sizeof(float2));
     return p;
 }
 
@@ -972,7 +978,7 @@ XP_API int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows,
     a.out_stride = out_stride;
     a.part = (float*)(ws + p.part);
     a.part_ml = (float*)(ws + p.ml);
-    a.lse = weights ? (float*)(ws + p.lse) : nullptr;
+    a.stats = weights ? (float2*)(ws + p.stats) : nullptr;
     a.weights = weights;
     a.w_stride = w_stride;
     a.heads = heads;

@@ -147,3 +147,51 @@ def test_prompt_f16_long_tail_of_small_weights(kv, group, dim, n, nats, spread):
     worst = float(((out.double() - want).abs() / want).max())
     print("relative error %.2e of %.2e" % (worst, rel), flush=True)
     assert worst <= rel
+
+
+@pytest.mark.parametrize("dim,group,q_rows,n", [(128, 1, 1, 300), (64, 8, 3, 5000), (256, 2, 1, 700)])
+@pytest.mark.parametrize("offset", [300.0, 3e3, 3e4, 3e5])
+def test_decode_weights_add_up_at_large_scores(offset, dim, group, q_rows, n):
+    """Scores of a few units of spread around a large offset (in log2 units): what a row adds to the weights is a
+    probability distribution, whatever the scores' size.
+
+    Both kernels form the same scores and take the same exponentials of their differences: two exponentials and
+    their arguments' roundings, 2^-20 in all; a lane's share of the sum is at most n / 4 fp32 adds, the rows' sum
+    at a position q_rows * group more."""
+    rng = np.random.default_rng(int(offset) + dim)
+    kv, page = 2, 64
+    cols = -(-n // page)
+    c = filled(rng, kv, dim, page, cols)
+    c.b[..., :1024] = 0x77                                 # group 0 of every key: 48 everywhere
+    c.b[..., c.ng * 1024:c.ng * 1024 + 64] = 0x50
+    table = tables(rng, 1, cols, cols)
+    q = rng.normal(size=(q_rows, kv * group, dim))
+    scale = 0.5 * dim ** -0.5
+    q[:, :, :32] = offset / (np.log2(np.e) * scale * 48.0 * 32.0) * rng.uniform(1.0, 1.2, (q_rows, kv * group, 1))
+    w = torch.zeros(1, kv, cols * page, device="cuda")
+    run_decode(c, on_device(c), table, np.array([n], dtype=np.int32), dev(q, torch.bfloat16), scale, q_rows=q_rows, weights=w)
+    total = w.double().sum(-1).cpu().numpy() / (q_rows * group)
+    bound = 2.0 ** -20 + (n / 4 + q_rows * group) * 2.0 ** -24
+    print("off by %.1e of %.1e" % (np.abs(total - 1).max(), bound), flush=True)
+    assert (np.abs(total - 1) <= bound).all(), total
+
+
+@pytest.mark.parametrize("ty,mag", [("f16", 32000.0), ("bf16", 1e6), ("bf16", 1e30)])
+def test_decode_weights_of_large_finite_scores(ty, mag):
+    """As test_decode_large_finite_scores: each row adds 1 at the position along which its query points."""
+    rng = np.random.default_rng(7)
+    kv, group, dim, page, n, q_rows = 2, 4, 128, 64, 4500, 2
+    cols = -(-n // page)
+    c = loud_cache(rng, kv, dim, page, cols)
+    table = tables(rng, 1, cols, cols)
+    q, want = np.zeros((q_rows, kv * group, dim)), np.zeros((1, kv, cols * page))
+    for h in range(kv):
+        k, _ = c.rows(table[0], h, n, "k")
+        for i in range(q_rows):
+            for g in range(group):
+                j = int(rng.integers(0, n - 1))
+                q[i, h * group + g] = np.sign(k[j]) * mag * rng.uniform(1.0, 2.0)
+                want[0, h, j] += 1.0
+    w = torch.zeros(1, kv, cols * page, device="cuda")
+    run_decode(c, on_device(c), table, np.array([n], dtype=np.int32), dev(q, DT[ty]), dim ** -0.5, q_rows=q_rows, weights=w)
+    np.testing.assert_array_equal(w.cpu().numpy(), want)
