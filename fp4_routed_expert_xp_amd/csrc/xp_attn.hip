@@ -311,9 +311,10 @@ __device__ __forceinline__ bool find_piece(const Args& a, int i, Piece& p) {
                 hit = __ballot(is_cut && first <= i && i < first + c.pieces * per);
                 i -= first;
             } else {
-                // eight classes of length, the longest first
+                // eight classes of length, the longest first (top + 1 is top from 2^24 on)
                 const int top = (int)wave_max_u32(in && !is_cut ? (uint32_t)c.tiles : 0u);
-                const int cls = in && !is_cut ? (top > 0 ? (int)(8.0f * (float)c.tiles / (float)(top + 1)) : 0) : -1;
+                const int part = top > 0 ? (int)(8.0f * (float)c.tiles / (float)(top + 1)) : 0;
+                const int cls = in && !is_cut ? (part > 7 ? 7 : part) : -1;
                 int before = 0;
 #pragma unroll
                 for (int k = 7; k >= 0; --k) {

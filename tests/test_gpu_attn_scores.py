@@ -195,3 +195,26 @@ def test_decode_weights_of_large_finite_scores(ty, mag):
     w = torch.zeros(1, kv, cols * page, device="cuda")
     run_decode(c, on_device(c), table, np.array([n], dtype=np.int32), dev(q, DT[ty]), dim ** -0.5, q_rows=q_rows, weights=w)
     np.testing.assert_array_equal(w.cpu().numpy(), want)
+
+
+def test_decode_a_sequence_of_2_30_positions_among_short_ones():
+    """The longest sequence of a batch that is worked on in order of length, of 2^24 tiles: a float no longer tells
+    its tiles from its tiles and one. All values are 1 and all scores equal, so every output is 1 exactly. Pages
+    that are only read may be shared: one page of 2^20 positions stands for all. max_len is smaller than the
+    longest length, as a launch may be, so nothing is cut."""
+    kv, page, batch, tile = 5, 1 << 20, 64, 2 * 2176
+    d = xp.kv_dims(kv, 64, page, 1)
+    one = torch.zeros(tile, dtype=torch.uint8)
+    one[2048:2176] = 0x38                                  # K: zeros
+    one[2176:2176 + 2048] = 0x22                           # V: ones
+    one[2176 + 2048:] = 0x38
+    buf = one.cuda().repeat(kv * (page // 64))
+    assert buf.numel() == xp.xp_kv_bytes(d)
+    table = torch.zeros(batch, 1 << 10, dtype=torch.int32, device="cuda")
+    lens = torch.arange(1, batch + 1, dtype=torch.int32, device="cuda")
+    lens[17] = 1 << 30
+    q = torch.randn(batch, kv, 64, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 3.0)
+    ws = torch.empty(xp.xp_attn_decode_workspace_bytes(d, kv, 1, batch, 1024), dtype=torch.uint8, device="cuda")
+    xp.xp_attn_decode(d, q, buf, table, lens, 1024, 0.125, out, ws)
+    assert (out == 1.0).all(), (out != 1.0).any(-1).nonzero().tolist()
