@@ -558,6 +558,7 @@ XP_API int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages,
     if (check_geo(dims, batch, dst_pages) != XP_OK || keep < 1 || sinks < 0 || recent < 0 ||
         (int64_t)sinks + recent > keep || keep > (int64_t)dst_pages * dims->page)
         return XP_ERR_SHAPE;
+    if (keep > (int64_t)0x80000000 - 8 * kSelThreads) return XP_ERR_SHAPE;   // indexes of the kernels' steps are ints
     if (batch == 0) return XP_OK;
     if (!cache || !table || !lens || !weights || !dst_table || !kept || !lens_out || !weights_out) return XP_ERR_NULL;
     if (w_stride < (int64_t)max_pages * dims->page || wo_stride < keep || !aligned_to(cache, 16) || !aligned_to(table, 4) ||

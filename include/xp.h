@@ -392,7 +392,8 @@ int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t
  * (xp_attn_decode's `weights`), for every kv head on its own. A sequence of at most
  * keep positions keeps all; a longer one keeps its first `sinks`, its last `recent`
  * and, between them, those of the largest weights (equal weights: lower positions
- * first; NaN below every number), all in their order. sinks + recent <= keep.
+ * first; NaN below every number), all in their order. sinks + recent <= keep <=
+ * 2^31 - 8192.
  *   kept        int32 [batch][kv_heads][keep]: the kept positions ascending, then -1;
  *   cache       the kept positions' codes and scales move to positions 0, 1, ... of
  *               dst_table [batch][dst_pages] in the same cache (room for keep positions);

@@ -218,3 +218,12 @@ def test_reference_attend_against_torch():
     assert (out[0] == 0).all() and (p[0] == 0).all()
     np.testing.assert_allclose(out[1], v[0])
     np.testing.assert_allclose(out[2], v[5])
+
+
+def test_evict_refuses_counts_that_its_steps_would_pass():
+    """The kernels' steps of up to 8,192 positions stay below 2^31 for at most 2^31 - 8192 kept ones."""
+    def call(keep):
+        pages = (2 ** 31 - 1025) // 64
+        return xp.lib().xp_kv_evict(kd(kv=1), 1, pages, P, P, P, P, 1 << 31, keep, 0, 0, pages, P, P, P, P, 1 << 31, None)
+    for keep in (2 ** 31 - 8191, 2 ** 31 - 4096, 2 ** 31 - 1088):
+        assert call(keep) == xp.XP_ERR_SHAPE, keep
