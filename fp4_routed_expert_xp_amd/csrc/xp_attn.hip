@@ -965,6 +965,9 @@ XP_API int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows,
         !kv::aligned_to(workspace, 16))
         return XP_ERR_SHAPE;
     if (weights && (w_stride < (int64_t)max_pages * dims->page || !kv::aligned_to(weights, 4))) return XP_ERR_SHAPE;
+    // a unit's q is read before its rows are written, but the weights kernel reads q again
+    const kv::Rows qr{q, (int64_t)batch * q_rows, 2 * q_stride, 2 * width}, yr{out, qr.n, 2 * out_stride, 2 * width};
+    if ((weights || !qr.same(yr)) && kv::rows_meet(qr, yr)) return XP_ERR_SHAPE;
     const Launch p = plan_of(dims, heads, q_rows, batch, max_len, window);
     if (ws_bytes < p.total) return XP_ERR_WORKSPACE;
     char* ws = (char*)workspace;

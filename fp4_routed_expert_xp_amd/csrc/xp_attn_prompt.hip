@@ -475,6 +475,11 @@ XP_API int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int
     if (q_stride < qw || out_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
         out_stride % 4 || !kv::aligned_to(q, 16) || !kv::aligned_to(k, 16) || !kv::aligned_to(v, 16) || !kv::aligned_to(out, 8) || !kv::aligned_to(cu_q, 4) || !kv::aligned_to(cu_k, 4))
         return XP_ERR_SHAPE;
+    // a workgroup's q is read before its rows are written; k and v are read by all
+    const kv::Rows qr{q, rows_q, 2 * q_stride, 2 * qw}, yr{out, rows_q, 2 * out_stride, 2 * qw};
+    if ((!qr.same(yr) && kv::rows_meet(qr, yr)) || kv::rows_meet(kv::Rows{k, rows_k, 2 * k_stride, 2 * kw}, yr) ||
+        kv::rows_meet(kv::Rows{v, rows_k, 2 * v_stride, 2 * kw}, yr))
+        return XP_ERR_SHAPE;
     const float f = kv::log2_scale(scale);
     const float lag = lag_of(type == XP_BF16) / f;
     const Args a{(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)out, q_stride, k_stride, v_stride,

@@ -535,6 +535,8 @@ XP_API int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, 
     const int st = check_rows(dims, batch, max_pages, rows, type, k, k_stride, v, v_stride, cu_rows, start, table, cache);
     if (st != XP_OK) return st;
     if (rows == 0 || batch == 0) return XP_OK;
+    const int64_t size = type == XP_F32 ? 4 : 2, width = (int64_t)dims->kv_heads * dims->head_dim * size;
+    if (rows_meet(Rows{k, rows, k_stride * size, width}, Rows{v, rows, v_stride * size, width})) return XP_ERR_SHAPE;
     const Geo g = geo_of(dims, max_pages);
     const RowMap m{cu_rows, start, table, batch, rows};
     hipStream_t s = (hipStream_t)stream;
@@ -565,11 +567,13 @@ XP_API int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages,
         !aligned_to(lens, 4) || !aligned_to(weights, 4) || !aligned_to(dst_table, 4) || !aligned_to(kept, 4) ||
         !aligned_to(lens_out, 4) || !aligned_to(weights_out, 4))
         return XP_ERR_SHAPE;
-    if (weights_out == weights && wo_stride != w_stride) return XP_ERR_SHAPE;   // rows would overlap others' sources
+    // in place a row's weights are read before they are written; other overlaps would meet other rows' sources
+    const int64_t most = (int64_t)max_pages * dims->page, n_rows = (int64_t)batch * dims->kv_heads;
+    const Rows wr{weights, n_rows, 4 * w_stride, 4 * most}, wor{weights_out, n_rows, 4 * wo_stride, 4 * (most < wo_stride ? most : wo_stride)};
+    if ((weights_out == weights && wo_stride != w_stride) || (!wr.same(wor) && rows_meet(wr, wor))) return XP_ERR_SHAPE;
     const Geo g = geo_of(dims, max_pages), d = geo_of(dims, dst_pages);
     hipStream_t s = (hipStream_t)stream;
     const int wo_len = wo_stride > 0x7fffffff ? 0x7fffffff : (int)wo_stride;
-    const int64_t most = (int64_t)max_pages * dims->page;
     const unsigned held = (unsigned)(most < kSelKeys ? most : kSelKeys) * sizeof(uint32_t);
     hipLaunchKernelGGL(evict_select_kernel, dim3(g.kv_heads, batch), dim3(kSelThreads), held, s, g, lens, weights,
                        (long long)w_stride, keep, sinks, recent, kept, weights_out, (long long)wo_stride, wo_len);

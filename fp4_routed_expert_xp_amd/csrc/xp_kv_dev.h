@@ -116,6 +116,38 @@ inline float log2_scale(float scale) {
     return (float)(x < 0x1p-126 ? 0x1p-126 : (x > 0x1p127 ? 0x1p127 : x));
 }
 
+// n rows of a buffer, `width` bytes each and `step` bytes apart (host).
+struct Rows {
+    const void* p;
+    int64_t n, step, width;
+    bool same(const Rows& o) const { return p == o.p && (step == o.step || n <= 1); }
+};
+// Whether two buffers' rows share a byte. Views into one wider buffer interleave without
+// sharing any; with one step the shift between rows decides it, otherwise a walk over both.
+inline bool rows_meet(const Rows& a, const Rows& b) {
+    typedef __int128 wide;
+    if (a.n < 1 || b.n < 1) return false;
+    const wide a0 = (wide)(uintptr_t)a.p, b0 = (wide)(uintptr_t)b.p, d = b0 - a0;
+    if (d >= (wide)(a.n - 1) * a.step + a.width || -d >= (wide)(b.n - 1) * b.step + b.width) return false;
+    if (a.step == b.step) {
+        // rows i of a and j of b meet where -b.width < d + (j - i) step < a.width
+        const auto floor_div = [](wide x, wide y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
+        const wide lo = floor_div(-b.width - d, a.step) + 1, hi = -floor_div(d - a.width, a.step) - 1;
+        return (lo > 1 - a.n ? lo : 1 - a.n) <= (hi < b.n - 1 ? hi : b.n - 1);
+    }
+    int64_t i = 0, j = 0;
+    while (i < a.n && j < b.n) {
+        const wide x = a0 + (wide)i * a.step, y = b0 + (wide)j * b.step;
+        if (x + a.width <= y)
+            i += (int64_t)((y - x - a.width) / a.step) + 1;
+        else if (y + b.width <= x)
+            j += (int64_t)((x - y - b.width) / b.step) + 1;
+        else
+            return true;
+    }
+    return false;
+}
+
 inline bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 }  // namespace kv

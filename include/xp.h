@@ -381,9 +381,9 @@ int xp_kv_append(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32
 
 /* The reverse, for the same row map: the cached values as `type` (any xp_type; all
  * three hold them exactly). Rows whose position the cache does not have are 0; rows
- * from cu_rows[batch] on are left as they were. For both calls kv_heads times the blocks
- * of 64 rows, a part of one counted whole, is below 2^24. A prompt's next piece reads
- * its prefix back with it for xp_attn_prompt. */
+ * from cu_rows[batch] on are left as they were. k and v must not overlap (XP_ERR_SHAPE).
+ * For both calls kv_heads times the blocks of 64 rows, a part of one counted whole, is
+ * below 2^24. A prompt's next piece reads its prefix back with it for xp_attn_prompt. */
 int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, int32_t type,
                const int32_t* cu_rows, const int32_t* start, const int32_t* table, const uint8_t* cache, void* k,
                int64_t k_stride, void* v, int64_t v_stride, void* stream);
@@ -399,7 +399,8 @@ int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t
  *               dst_table [batch][dst_pages] in the same cache (room for keep positions);
  *   lens_out    int32 [batch]: min(lens, keep); may be lens;
  *   weights_out fp32 [batch][kv_heads] rows of wo_stride: the kept weights, then 0 up to
- *               the old length (or the row's end); may be weights, with the same stride.
+ *               the old length (or the row's end); may be weights, with the same stride,
+ *               and must not overlap them otherwise (XP_ERR_SHAPE).
  * The destination pages are either the source's own, entry for entry (as far as they
  * go), or pages that no source entry names. weights: rows of w_stride >= max_pages *
  * page fp32. lens are taken as between 0 and max_pages * page. */
@@ -429,6 +430,8 @@ size_t xp_attn_decode_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int
  * should exceed it, and one that does is computed all the same, only slower.
  * weights (or NULL): fp32 [batch][kv_heads] rows of w_stride >= max_pages * page; the
  * call adds to each position the probabilities of all the kv head's rows there.
+ * Without weights out may be q itself, with the same stride; otherwise rows of out must
+ * not overlap rows of q (XP_ERR_SHAPE).
  * workspace: 16-byte aligned, needs no initial value; calls that share it must not
  * overlap. Results do not depend on the launch's timing. heads * q_rows is at most 2^24,
  * batch times the kv heads' blocks of 16 rows at most 2^22. */
@@ -443,7 +446,8 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
  * cu_q[b] .. cu_q[b+1] - 1 of q and out and cu_k[b] .. cu_k[b+1] - 1 of k and v.
  * Its last query sits at its last key's position, so a prompt's later piece may
  * attend to the earlier pieces' keys; a query before its first key sees nothing.
- * Rows of out from cu_q[batch] on are left as they were. Strides of k and v are below
+ * Rows of out from cu_q[batch] on are left as they were. out may be q itself, with the
+ * same stride; otherwise its rows must not overlap rows of q, k or v (XP_ERR_SHAPE). Strides of k and v are below
  * 2^24 elements, rows_q * heads below 2^29. */
 int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch, int32_t rows_q, int32_t rows_k,
                    int32_t type, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

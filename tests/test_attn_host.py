@@ -227,3 +227,59 @@ def test_evict_refuses_counts_that_its_steps_would_pass():
         return xp.lib().xp_kv_evict(kd(kv=1), 1, pages, P, P, P, P, 1 << 31, keep, 0, 0, pages, P, P, P, P, 1 << 31, None)
     for keep in (2 ** 31 - 8191, 2 ** 31 - 4096, 2 ** 31 - 1088):
         assert call(keep) == xp.XP_ERR_SHAPE, keep
+
+
+def _share(a, sa, b, sb, rows, width):
+    """Whether rows of `width` bytes at a, a + sa, ... and b, b + sb, ... share a byte."""
+    return any(a + i * sa < b + j * sb + width and b + j * sb < a + i * sa + width for i in range(rows) for j in range(rows))
+
+
+def test_decode_refuses_out_over_q():
+    """Where rows meet, also rows of another stride; views that interleave without meeting pass (to the workspace
+    check, which these calls fail)."""
+    base, width = 1 << 20, 256
+    rng = np.random.default_rng(0)
+    seen = set()
+    for _ in range(3000):
+        rows = int(rng.integers(1, 6))
+        qs, os_ = (int(rng.integers(32, 120)) * 8 for _ in "qo")
+        if rng.random() < 0.5:
+            os_ = qs
+        out = base + 16 * int(rng.integers(-600, 600))
+        for weights in (None, P):
+            same = out == base and (os_ == qs or rows == 1)
+            bad = (weights is not None or not same) and _share(base, 2 * qs, out, 2 * os_, rows, 2 * width)
+            got = _decode(q_rows=rows, q=ctypes.c_void_p(base), qs=qs, out=ctypes.c_void_p(out), os=os_, weights=weights,
+                          ws=64, bytes=0)
+            assert got == (xp.XP_ERR_SHAPE if bad else xp.XP_ERR_WORKSPACE), (rows, qs, os_, out - base, weights)
+            seen.add((bad, os_ == qs))
+    assert len(seen) == 4
+    at = ctypes.c_void_p(base)
+    assert _decode(q_rows=3, q=at, out=at, bytes=0) == xp.XP_ERR_WORKSPACE
+    assert _decode(q_rows=3, q=at, out=at, os=512, bytes=0) == xp.XP_ERR_SHAPE
+    assert _decode(q_rows=3, q=at, out=at, weights=P, ws=64, bytes=0) == xp.XP_ERR_SHAPE
+    far = 1 << 60
+    assert _decode(q_rows=3, q=at, qs=far, out=ctypes.c_void_p(base + 16), os=far, bytes=0) == xp.XP_ERR_SHAPE
+    assert _decode(q_rows=3, q=at, qs=far, out=ctypes.c_void_p(base + 512), os=far, bytes=0) == xp.XP_ERR_WORKSPACE
+
+
+def test_other_calls_refuse_what_they_write_over_what_they_read():
+    L, c = xp.lib(), ctypes.c_void_p
+    at = 1 << 20
+
+    def prompt(out, os_=256):
+        return L.xp_attn_prompt(4, 2, 64, 1, 5, 5, BF16, c(at), 256, c(at + (1 << 16)), 128, c(at + (2 << 16)), 128, P, P, 1.0,
+                                0, c(out), os_, None)
+    for out in (at + 16, at - 512, at + 4 * 512 + 496, at + (1 << 16), at + (1 << 16) + 4 * 256 + 240, at + (2 << 16) - 2048):
+        assert prompt(out) == xp.XP_ERR_SHAPE, out - at
+    assert prompt(at, 512) == xp.XP_ERR_SHAPE
+
+    def read(v, vs=128):
+        return _rows_call("xp_kv_read", k=c(at), v=c(v), vs=vs)
+    for v, vs in ((at, 128), (at + 16, 128), (at - 256 * 2, 128), (at - 256 * 2, 192)):
+        assert read(v, vs) == xp.XP_ERR_SHAPE, v - at
+
+    def evict(wo, wos=128):
+        return L.xp_kv_evict(kd(), 2, 2, P, P, P, c(at), 128, 64, 0, 0, 1, P, P, P, c(wo), wos, None)
+    for wo, wos in ((at + 4, 128), (at - 4 * 4 * 128 + 512, 128), (at + 512, 64), (at + 4 * 512 - 4, 128), (at, 256)):
+        assert evict(wo, wos) == xp.XP_ERR_SHAPE, (wo - at, wos)

@@ -845,3 +845,42 @@ def test_refusals_on_device_tensors():
         xp.xp_attn_decode(d, q, buf, t, st, 128, -1.0, q.clone(), ws)
     with pytest.raises(ValueError):
         xp.xp_attn_prompt(q, x, x.half(), cu, cu, 1.0, q.clone())
+
+
+def test_out_on_q_and_beside_it():
+    """out may be q itself (without weights), and rows of one wider buffer may hold both beside each other."""
+    rng = np.random.default_rng(17)
+    kv, dim, page, n = 2, 64, 64, 3000
+    c = filled(rng, kv, dim, page, 120)
+    table = tables(rng, 2, 47, 94)
+    d, buf, t = dims_of(c), on_device(c), dev(table)
+    for lens in ([n, 2900], [100, 40]):                    # cut and whole
+        size, ln = max(lens), ints(lens)
+        ws = torch.empty(xp.xp_attn_decode_workspace_bytes(d, 8, 3, 2, size), dtype=torch.uint8, device="cuda")
+        wide = dev(rng.normal(size=(6, 16, dim)), torch.bfloat16)
+        q, o = wide[:, 3:11].clone(), torch.empty(6, 8, dim, dtype=torch.bfloat16, device="cuda")
+        xp.xp_attn_decode(d, q, buf, t, ln, size, 0.125, o, ws, q_rows=3)
+        xp.xp_attn_decode(d, q, buf, t, ln, size, 0.125, q, ws, q_rows=3)
+        assert torch.equal(q, o)
+        xp.xp_attn_decode(d, wide[:, :8], buf, t, ln, size, 0.125, wide[:, 8:], ws, q_rows=3,
+                          weights=torch.zeros(2, kv, 47 * page, device="cuda"))
+        xp.xp_attn_decode(d, wide[:, :8], buf, t, ln, size, 0.125, o, ws, q_rows=3)
+        assert torch.equal(wide[:, 8:], o)
+        for w in (None, torch.zeros(2, kv, 47 * page, device="cuda")):
+            with pytest.raises(xp.XPError):
+                xp.xp_attn_decode(d, wide[:, :8], buf, t, ln, size, 0.125, wide[:, 7:15], ws, q_rows=3, weights=w)
+        with pytest.raises(xp.XPError):
+            xp.xp_attn_decode(d, q, buf, t, ln, size, 0.125, q, ws, q_rows=3, weights=torch.zeros(2, kv, 47 * page, device="cuda"))
+    cu = dev(ends([150, 61]))
+    for group, heads_kv in ((2, 2), (2, 100)):             # both forms
+        wide = dev(rng.normal(size=(211, heads_kv * (2 * group + 2), dim)), torch.float16)
+        h = heads_kv * group
+        q, k, v, at = wide[:, :h], wide[:, h:h + heads_kv], wide[:, h + heads_kv:h + 2 * heads_kv], wide[:, h + 2 * heads_kv:]
+        o = torch.empty(211, h, dim, dtype=torch.float16, device="cuda")
+        xp.xp_attn_prompt(q, k, v, cu, cu, 0.125, o)
+        xp.xp_attn_prompt(q, k, v, cu, cu, 0.125, at)
+        xp.xp_attn_prompt(q, k, v, cu, cu, 0.125, q)
+        assert torch.equal(at, o) and torch.equal(q, o)
+        for bad in (wide[:, 1:1 + h], wide[:, h - 1:2 * h - 1], wide[:, 2 * heads_kv:2 * heads_kv + h]):
+            with pytest.raises(xp.XPError):
+                xp.xp_attn_prompt(q, k, v, cu, cu, 0.125, bad)
