@@ -908,7 +908,7 @@ static int check_decode(const xp_kv_dims* d, int heads, int q_rows, int batch, i
     if (heads < 1 || heads > 65535 || heads % d->kv_heads || q_rows < 1 || q_rows > 65535 || max_len < 0) return XP_ERR_SHAPE;
     if ((long long)heads * q_rows > (1 << 24)) return XP_ERR_SHAPE;     // rows of a sequence fit an int
     const Launch p = plan_of(d, heads, q_rows, batch, max_len, 0);
-    if (p.units + p.share > (1 << 22)) return XP_ERR_SHAPE;             // a launch has fewer than 2^32 threads
+    if (p.units > (1 << 22)) return XP_ERR_SHAPE;   // four waves each then: a launch has fewer than 2^32 threads
     return XP_OK;
 }
 

@@ -434,7 +434,8 @@ size_t xp_attn_decode_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int
  * not overlap rows of q (XP_ERR_SHAPE).
  * workspace: 16-byte aligned, needs no initial value; calls that share it must not
  * overlap. Results do not depend on the launch's timing. heads * q_rows is at most 2^24,
- * batch times the kv heads' blocks of 16 rows at most 2^22. */
+ * batch times the kv heads' blocks of 16 rows (of 32 where a kv head has more than 16 and
+ * head_dim is below 256) at most 2^22. */
 int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_t batch, int32_t max_pages,
                    int32_t max_len, int32_t type, const void* q, int64_t q_stride, float scale, int32_t window,
                    const uint8_t* cache, const int32_t* table, const int32_t* lens, void* out, int64_t out_stride,
@@ -448,7 +449,8 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
  * attend to the earlier pieces' keys; a query before its first key sees nothing.
  * Rows of out from cu_q[batch] on are left as they were. out may be q itself, with the
  * same stride; otherwise its rows must not overlap rows of q, k or v (XP_ERR_SHAPE). Strides of k and v are below
- * 2^24 elements, rows_q * heads below 2^29. */
+ * 2^24 elements; with g = heads / kv_heads, (rows_q * g / 64, rounded up, + batch) *
+ * kv_heads is below 2^23. */
 int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch, int32_t rows_q, int32_t rows_k,
                    int32_t type, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                    int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, float scale, int32_t window, void* out,

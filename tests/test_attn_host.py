@@ -283,3 +283,30 @@ def test_other_calls_refuse_what_they_write_over_what_they_read():
         return L.xp_kv_evict(kd(), 2, 2, P, P, P, c(at), 128, 64, 0, 0, 1, P, P, P, c(wo), wos, None)
     for wo, wos in ((at + 4, 128), (at - 4 * 4 * 128 + 512, 128), (at + 512, 64), (at + 4 * 512 - 4, 128), (at, 256)):
         assert evict(wo, wos) == xp.XP_ERR_SHAPE, (wo - at, wos)
+
+
+def test_decode_takes_2_22_units_at_any_length():
+    """Units: blocks of 16 rows of a kv head, of 32 where it has more than 16 and head_dim is below 256."""
+    for dim, heads, q_rows, batch in ((64, 1024, 1, 4096), (128, 1024, 16, 4096), (256, 1024, 16, 4096), (64, 1024, 32, 4096),
+                                      (128, 2048, 16, 4096), (256, 1024, 32, 2048), (64, 1024, 33, 2048)):
+        d = xp.kv_dims(1024, dim, 64, 4)
+        for max_len in (0, 64, 20000, 1 << 30):
+            assert xp.xp_attn_decode_workspace_bytes(d, heads, q_rows, batch, max_len) > 0, (dim, heads, q_rows, max_len)
+            assert xp.xp_attn_decode_workspace_bytes(d, heads, q_rows, batch + 1, max_len) == 0, (dim, heads, q_rows, max_len)
+            call = dict(g=ctypes.byref(d), heads=heads, q_rows=q_rows, max_len=max_len, qs=heads * dim, os=heads * dim,
+                        out=ctypes.c_void_p(1 << 50), bytes=0)
+            assert _decode(batch=batch, **call) == xp.XP_ERR_WORKSPACE
+            assert _decode(batch=batch + 1, **call) == xp.XP_ERR_SHAPE
+
+
+def test_prompt_takes_fewer_than_2_23_blocks():
+    """Blocks of 64 rows of a kv head, rows_q * heads / kv_heads of them for each, and one more for each sequence."""
+    def call(heads, kv, batch, rq):
+        return xp.lib().xp_attn_prompt(heads, kv, 64, batch, rq, 5, BF16, None, 1 << 20, P, 1 << 20, P, 1 << 20, P, P, 1.0, 0,
+                                       P, 1 << 20, None)
+    for heads, kv, batch, rq in ((1024, 1024, 1, 64 * 8190), (2048, 1024, 1, 32 * 8190), (128, 128, 65535, 0),
+                                 (1, 1, 1, 64 * (2 ** 23 - 2)), (129, 129, 60000, 64 * 5027)):
+        blocks = (-(-rq * (heads // kv) // 64) + batch) * kv
+        assert blocks + kv >= 1 << 23 > blocks
+        assert call(heads, kv, batch, rq) == (xp.XP_ERR_NULL if rq else xp.XP_OK), (heads, kv, batch, rq)
+        assert call(heads, kv, batch, rq + 64 * kv // heads) == xp.XP_ERR_SHAPE, (heads, kv, batch, rq)
