@@ -10,6 +10,7 @@ import torch
 from fp4_routed_expert_xp_amd import xp
 
 import attn_ref as ref
+import attn_tiles as tiles
 
 P = ctypes.c_void_p(0x1000)
 ODD = ctypes.c_void_p(0x1004)
@@ -310,3 +311,33 @@ def test_prompt_takes_fewer_than_2_23_blocks():
         assert blocks + kv >= 1 << 23 > blocks
         assert call(heads, kv, batch, rq) == (xp.XP_ERR_NULL if rq else xp.XP_OK), (heads, kv, batch, rq)
         assert call(heads, kv, batch, rq + 64 * kv // heads) == xp.XP_ERR_SHAPE, (heads, kv, batch, rq)
+
+
+@pytest.mark.parametrize("name", list(tiles.DECODE) + list(tiles.PROMPT))
+def test_a_tile_left_out_or_doubled_is_told(name):
+    """For the rows of the cases of attn_tiles (some of those where there are many), but for tiles of which a row
+    sees fewer than eight positions."""
+    if name in tiles.DECODE:
+        case = tiles.DECODE[name]
+        dim, window, places = case[2], case[5], sorted({p for _, _, p in tiles.decode_rows(case)})
+    else:
+        case = tiles.PROMPT[name]
+        dim, window, places = case[2], case[5], [p for _, p in tiles.prompt_rows(case)]
+    for place in places if len(places) <= 12 else places[::len(places) // 6]:
+        c = tiles.counts(place, window)
+        assert c.sum() == max(0, min(place + 1, window or place + 1))
+        if np.count_nonzero(c) > 1:                        # one alone is all of the output, once or twice
+            assert all(c[t] < 8 for t in tiles.not_told_apart(c, dim)), place
+
+
+def test_the_tiles_form_of_attention():
+    """Its closed form is the definition's: equal scores over values that name their tile."""
+    for dim, at, window in ((64, 700, 0), (64, 5000, 0), (128, 400, 150)):
+        n = at + 1
+        col, val = tiles.column(np.arange(n) // 64, dim)
+        v = np.zeros((n, dim))
+        v[np.arange(n), col] = tiles.VALUES[val]
+        out, _, _, _ = ref.attend(np.ones((1, dim)), np.ones((n, dim)), v, [at], 0.1, window)
+        np.testing.assert_allclose(tiles.output(tiles.counts(at, window), dim), out[0], rtol=1e-12)
+    codes = ref.E2M1[tiles.CODES]
+    np.testing.assert_array_equal(codes, tiles.VALUES)
