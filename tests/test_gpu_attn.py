@@ -884,3 +884,33 @@ def test_out_on_q_and_beside_it():
         for bad in (wide[:, 1:1 + h], wide[:, h - 1:2 * h - 1], wide[:, 2 * heads_kv:2 * heads_kv + h]):
             with pytest.raises(xp.XPError):
                 xp.xp_attn_prompt(q, k, v, cu, cu, 0.125, bad)
+
+
+@pytest.mark.parametrize("kv,group,dim,ty", [(2, 4, 128, "bf16"), (1, 2, 64, "f16"), (2, 2, 256, "bf16")])
+def test_prompt_in_two_pieces_over_the_cache(kv, group, dim, ty):
+    """The way of a prompt's later piece: both pieces' rows go into the cache as they come, the keys and values of
+    all of it are read back, and the new rows attend to them; as tokens of a decode call they see the same."""
+    rng = np.random.default_rng(dim)
+    page, first, then = 64, [130, 0, 70], [45, 33, 1]
+    rows, cols = [a + b for a, b in zip(first, then)], 3
+    c = ref.Cache(kv, dim, page, 3 * cols, rng=rng)
+    table = tables(rng, 3, cols, 3 * cols)
+    d, buf, t = dims_of(c), on_device(c), dev(table)
+    k, v = (dev(rng.normal(size=(sum(rows), kv, dim)), DT[ty]) for _ in "kv")
+    q = dev(rng.normal(size=(sum(then), kv * group, dim)), DT[ty])
+    cu, cu_q = ends(rows), ends(then)
+    old = torch.from_numpy(np.concatenate([np.arange(cu[b], cu[b] + first[b]) for b in range(3)])).cuda()
+    new = torch.from_numpy(np.concatenate([np.arange(cu[b] + first[b], cu[b + 1]) for b in range(3)])).cuda()
+    xp.xp_kv_append(d, k[old], v[old], dev(ends(first)), ints([0, 0, 0]), t, buf)
+    xp.xp_kv_append(d, k[new], v[new], dev(cu_q), ints(first), t, buf)
+    kr, vr = torch.empty_like(k), torch.empty_like(v)
+    xp.xp_kv_read(d, dev(cu), ints([0, 0, 0]), t, buf, kr, vr)
+    out = torch.empty_like(q)
+    xp.xp_attn_prompt(q, kr, vr, dev(cu_q), dev(cu), dim ** -0.5, out)
+    check_prompt(q, kr, vr, cu_q, cu, out, dim ** -0.5)
+    ref.append(c, k.double().cpu().numpy(), v.double().cpu().numpy(), cu, [0, 0, 0], table)
+    np.testing.assert_array_equal(buf.cpu().numpy(), c.b.reshape(-1))
+    for b in range(3):                                     # the same rows as tokens of a decode call
+        o = run_decode(c, buf, table[b:b + 1], np.array([rows[b]], dtype=np.int32), q[cu_q[b]:cu_q[b + 1]], dim ** -0.5,
+                       q_rows=then[b])
+        check_decode(c, table[b:b + 1], np.array([rows[b]]), q[cu_q[b]:cu_q[b + 1]], o, dim ** -0.5, 0, then[b])

@@ -218,3 +218,40 @@ def test_decode_a_sequence_of_2_30_positions_among_short_ones():
     ws = torch.empty(xp.xp_attn_decode_workspace_bytes(d, kv, 1, batch, 1024), dtype=torch.uint8, device="cuda")
     xp.xp_attn_decode(d, q, buf, table, lens, 1024, 0.125, out, ws)
     assert (out == 1.0).all(), (out != 1.0).any(-1).nonzero().tolist()
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16"])
+@pytest.mark.parametrize("kv,group,dim", [(1, 2, 64), (1, 2, 128), (1, 1, 256), (64, 2, 64), (64, 2, 128)])
+@pytest.mark.parametrize("climb", [0.6, 1.9, 2.1, 7.8, 8.2, 30.0, -3.0])
+def test_prompt_scores_that_climb_from_tile_to_tile(climb, kv, group, dim, ty):
+    """By less and by more than the running maximum may lag behind, in powers of two a tile, over 20 tiles: it is
+    raised never, now and then, or at every tile.
+
+    Scores are one product each. The bound: half a step of the output; a rounding of each weight in the products and
+    in the sum; fp16 weights below its normal numbers, 2^-38 of the largest each, in both; fp32 sums of n terms, the
+    maximum's product with the factor and the exponential, n 2^-24 + 2^-16 + 2^-19."""
+    rng = np.random.default_rng(dim + kv)
+    n, rows = 1290, 150
+    half = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[ty]
+    k = np.zeros((n, kv, dim))
+    k[:, :, 0] = climb * (np.arange(n) // 64)[:, None] + rng.uniform(-0.5, 0.5, (n, kv))
+    v = rng.normal(size=k.shape)
+    q = np.zeros((rows, kv * group, dim))
+    q[:, :, 0] = 1.0
+    q, k, v = (dev(x, DT[ty]) for x in (q, k, v))
+    out = torch.empty_like(q)
+    xp.xp_attn_prompt(q, k, v, dev(ends([rows])), dev(ends([n])), float(np.log(2.0)), out)
+    kd, vd, got = k.double().cpu().numpy(), v.double().cpu().numpy(), out.double().cpu().numpy()
+    worst = 0.0
+    for h in sorted({0, kv // 2, kv - 1}):
+        s = np.where(np.arange(n)[None, :] <= np.arange(n - rows, n)[:, None], kd[:, h, 0] * np.log(2.0), -np.inf)
+        e = np.exp(s - s.max(1, keepdims=True))
+        p = e / e.sum(1, keepdims=True)
+        want, wide = p @ vd[:, h], p @ np.abs(vd[:, h])
+        tol = half * np.abs(want) + (half + n * 2.0 ** -24 + 2.0 ** -16 + 2.0 ** -19) * (wide + np.abs(want))
+        tol += (2.0 ** -38 if ty == "f16" else 0.0) * (np.abs(vd[:, h]).sum(0) + n * np.abs(want)) + 1e-30
+        for g in range(group):
+            err = np.abs(got[:, h * group + g] - want)
+            assert (err <= tol).all(), (h, g, float((err / tol).max()))
+            worst = max(worst, float((err / tol).max()))
+    print("share of the bound: %.2f" % worst, flush=True)
