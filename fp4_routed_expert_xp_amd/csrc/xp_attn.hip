@@ -662,6 +662,8 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) l[mt] = sum_over_q(l[mt]);
     __syncthreads();                                       // the regions are read
+    int quarter = q;                                       // q, formed again: held over the loop, what is
+    asm volatile("" : "+v"(quarter));                      // derived from it spills 64 columns' 128 registers
     {
         f32x4* buf = (f32x4*)(lds + wave * join_bytes<D, MT>());
         float* ml = (float*)(buf + MT * NH * 64);
@@ -707,7 +709,7 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
         const int tok = r / a.group, hd = head * a.group + r - tok * a.group;
         uint16_t* y = (uint16_t*)a.out + ((long long)b * a.q_rows + tok) * a.out_stride + (long long)hd * D;
         const float inv = jl == 0.0f ? 0.0f : 1.0f / jl;   // nothing seen: zeros
-        *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(acc * inv);
+        *(uint2*)(y + 16 * h + 4 * quarter) = to16<BF16>(acc * inv);
         if (a.stats && h == 0 && q == 0) a.stats[((long long)b * a.heads + head * a.group) * a.q_rows + r] = stats_of(jm, jl);
     }
 }
