@@ -402,10 +402,13 @@ __device__ __forceinline__ uint2 to16(f32x4 v) {
     }
 }
 
-// Waves a CU holds at once, by registers: also the most a workgroup takes.
+// Waves a CU holds at once, by registers: also the most a workgroup takes. At 64 columns 131,072
+// positions of 4 kv heads take 21.7 us in 16 and 20.0 in 12, 16 sequences to 2,500 positions 12.8
+// and 14.1. Two sixteens of rows at 128 columns take 238 registers in 8 (16 sequences to 8,192
+// positions, 8 kv heads, 40 rows: 59 us) and, left to grow, 324 in 4 (85 us).
 template <int D, int MT>
 constexpr int waves_per_cu() {
-    return MT == 1 ? (D == 64 ? 16 : (D == 128 ? 12 : 8)) : (D == 64 ? 8 : 4);
+    return MT == 1 ? (D == 64 ? 16 : (D == 128 ? 12 : 8)) : 8;
 }
 template <int D, int MT>
 constexpr int region_bytes() {
@@ -857,7 +860,11 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
     }
 }
 
-// Rows of a block: 16 * MT.
+// Rows of a block: 16 * MT. Two sixteens read a tile's bytes once and decode them once for both,
+// with half as many registers again. 16 sequences to 8,192 positions of 8 kv heads, 128 columns, 32
+// rows a kv head: 39 us (43 in blocks of 16); 40 rows: 59 (60); one of 65,536: 31 (33); at 64
+// columns 27 (28). Where there are units enough without, blocks of 16 are faster: 32 sequences
+// to 4,096 42 us (37), eight to 700 12.6 (10.5). At 256 columns two exceed the registers.
 static int row_tiles(int rows, int dim) { return rows <= 16 || dim == 256 ? 1 : 2; }
 
 constexpr int kCus = 256;
