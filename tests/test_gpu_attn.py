@@ -914,3 +914,40 @@ def test_prompt_in_two_pieces_over_the_cache(kv, group, dim, ty):
         o = run_decode(c, buf, table[b:b + 1], np.array([rows[b]], dtype=np.int32), q[cu_q[b]:cu_q[b + 1]], dim ** -0.5,
                        q_rows=then[b])
         check_decode(c, table[b:b + 1], np.array([rows[b]]), q[cu_q[b]:cu_q[b + 1]], o, dim ** -0.5, 0, then[b])
+
+
+def test_a_cache_of_more_than_4_gib():
+    """Pages far apart in a large cache: the same calls over the same bytes in a small one give the same."""
+    rng = np.random.default_rng(13)
+    kv, dim, page, far = 2, 256, 1 << 15, 290                 # 17.8 MB a page: the last ones beyond 2^32 and 5e9 bytes
+    small, large = xp.kv_dims(kv, dim, page, 4), xp.kv_dims(kv, dim, page, far)
+    assert xp.xp_kv_bytes(large) > 5 * 10 ** 9
+    ids = np.array([[240, 0], [289, 241]], dtype=np.int32)      # page 240 crosses 2^32
+    one = xp.xp_kv_bytes(small) // 4
+    assert 240 * one < 2 ** 32 < 241 * one
+    n = [page + 700, page + 77]
+    cu, cu1, start = ends(n), ends([1, 1]), [0, 0]
+    k, v = (torch.randn(int(cu[-1]), kv, dim, device="cuda").to(torch.bfloat16) for _ in "kv")
+    q = torch.randn(2, 8, dim, device="cuda").to(torch.bfloat16)
+    w0 = torch.rand(2, kv, 2 * page, device="cuda")
+    got = []
+    for d, table in ((small, np.array([[0, 1], [2, 3]], dtype=np.int32)), (large, ids)):
+        buf = torch.zeros(xp.xp_kv_bytes(d), dtype=torch.uint8, device="cuda")
+        t, ln, w = dev(table), ints(n), w0.clone()
+        xp.xp_kv_append(d, k, v, dev(cu), ints(start), t, buf)
+        xp.xp_kv_append(d, k[:2], v[:2], dev(cu1), ints([n[0] - 1, n[1] - 1]), t, buf)   # the form for few rows
+        ws = torch.empty(xp.xp_attn_decode_workspace_bytes(d, 8, 1, 2, max(n)), dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        xp.xp_attn_decode(d, q, buf, t, ln, max(n), 0.06, out, ws, weights=w)
+        kept = torch.empty(2, kv, page + 5, dtype=torch.int32, device="cuda")
+        wk = w.clone()
+        xp.xp_kv_evict(d, buf, t, ln, w, page + 5, t, kept, ln, w, sinks=4, recent=8)
+        ko, vo = (torch.empty(2 * (page + 5), kv, dim, dtype=torch.float32, device="cuda") for _ in "kv")
+        xp.xp_kv_read(d, dev(ends([page + 5] * 2)), ints(start), t, buf, ko, vo)
+        k1, v1 = (torch.empty(2, kv, dim, dtype=torch.float32, device="cuda") for _ in "kv")
+        xp.xp_kv_read(d, dev(cu1), ints([page + 4, page + 4]), t, buf, k1, v1)
+        got.append((out, wk, w, kept, ln, ko, vo, k1, v1))
+        del buf
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert (got[0][0] != 0).any() and (got[0][5] != 0).any() and torch.equal(got[0][7], got[0][5][[page + 4, 2 * page + 9]])
