@@ -10,7 +10,7 @@ ABI. The round is captured once as a HIP graph and replayed; all weights
 The headline is the one-row workload on the two-launch path (xp_route_gateup,
 xp_down_combine); every workload is also timed on the four-call path, and the
 four-row same-expert and sixteen-row random workloads are extra cells on the
-same line.
+same line, by their main figures; every cell's whole report goes to stderr.
 Prints ONE JSON line.
 """
 from __future__ import annotations
@@ -79,6 +79,14 @@ def measured_traffic(t=None, sources=ROOFLINE_SOURCES):
 
 def log(msg: str) -> None:
     print("[bench] " + msg, file=sys.stderr, flush=True)
+
+
+# A cell's figures on the line, so that the line stays one that a log keeps whole.
+BRIEF = ("rows_per_s", "layer_us", "us", "tflops", "pct_hbm_peak")
+
+
+def brief(reports: dict) -> dict:
+    return {key: {f: rep[f] for f in BRIEF if f in rep} for key, rep in reports.items()}
 
 
 def parse():
@@ -793,7 +801,7 @@ def main():
         "copy_gbps": round(copy_gbps, 1),
         "decode_pct_hbm_peak": decode_pct(reports),
         "wall_s_timed": round(th["wall_s"], 4),
-        "cells": reports,
+        "cells": brief(reports),
     }
     dn_kernel = "down_combine_one_row_kernel (xp_down_combine)" if head["rows"] == 1 else (
         "down_combine_rows_kernel (xp_down_combine)" if head["rows"] * base.k <= 64

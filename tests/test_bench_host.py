@@ -1,4 +1,5 @@
 """bench.py on the host: the one-GPU contract and its accounting (no GPU needed)."""
+import json
 import os
 import subprocess
 import sys
@@ -46,3 +47,15 @@ def test_sweep_sets_are_valid_pass_sizes():
     for gu, dn in bench.TIER_SWEEP:
         for t in (gu, dn):
             assert list(t) == sorted(set(t)) and all(2 <= v <= 8 for v in t)
+
+
+def test_the_line_names_every_cell_briefly():
+    """Whole reports of the default cells made the line longer than the 16,000 characters that a log keeps of it."""
+    rep = dict(workload="sixteen_random", path="two_calls", rows_per_s=1484.83, layer_us=269.392, pct_hbm_peak=63.17,
+               kernel_us={"route": 5.6}, tflops=751.9)
+    reports = {"sixteen_random/two_calls/tiers_gu2-4-6-8_dn2-4/%d" % i: rep for i in range(40)}
+    reports["attention/prompt"] = dict(rows=4096, us=186.17, tflops=738.4)
+    b = bench.brief(reports)
+    assert list(b) == list(reports) and b["attention/prompt"] == dict(us=186.17, tflops=738.4)
+    assert all(set(v) <= set(bench.BRIEF) and v for v in b.values())
+    assert len(json.dumps(b)) < 8000
