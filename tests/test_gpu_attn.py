@@ -951,3 +951,12 @@ def test_a_cache_of_more_than_4_gib():
     for a, b in zip(*got):
         assert torch.equal(a, b)
     assert (got[0][0] != 0).any() and (got[0][5] != 0).any() and torch.equal(got[0][7], got[0][5][[page + 4, 2 * page + 9]])
+
+
+def test_bench_attention_cell():
+    import bench
+    r = bench.time_attn(2, 3, 1)
+    assert set(r) == {"attention/%d" % n for n in bench.ATTN_ROWS} | {"attention/prompt"}
+    b = bench.brief(r)
+    assert all(v["layer_us"] > 0 for k, v in b.items() if k != "attention/prompt")
+    assert b["attention/prompt"]["us"] > 0 and b["attention/prompt"]["tflops"] > 0
