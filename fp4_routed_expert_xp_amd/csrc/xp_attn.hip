@@ -23,10 +23,12 @@
 // fp16's normal numbers is then within 2^-40 of the row's largest.
 //
 // Bound by the cache's bytes where contexts are long: 64 ragged sequences to 8,192
-// positions (8 kv heads of 128, 313 MB) take 78 us, 4.0 TB/s, 1.005 times the bytes
+// positions (8 kv heads of 128, 313 MB) take 79 us, 4.0 TB/s, 1.005 times the bytes
 // fetched; 64 equal ones of 18,432 positions run at 5.7 TB/s. What is lost is mostly the
-// longest sequence's chain of tiles, about 2.3 us each for its wave. Per tile and wave
-// the vector pipe issues some 420 instructions (256 of them decode codes and scales)
+// longest sequence's chain of tiles, about 2.3 us each for its wave. The next tile's page
+// number is part of that chain: it is loaded at the top of a tile and waited for, and with
+// it the tile's V, which is needed only behind the scores. Per tile and wave
+// the vector pipe issues some 440 instructions (256 of them decode codes and scales)
 // and the matrix pipe 32 products: about half of the memory's time. Short calls are
 // bound by the chain length -> page -> bytes -> products -> join, 8 us in all.
 #include "xp_kv_dev.h"
@@ -464,7 +466,8 @@ __global__ __launch_bounds__((64 * waves_per_cu<D, MT>())) void attn_decode_kern
     // positions that every row sees
     const int full_lo = span_of(a, len, last_row).lo, full_hi = span_of(a, len, first_row).hi;
 
-    // a tile's bytes, loaded one tile ahead: K once its scores are formed, V once it is in LDS
+    // a tile's bytes, asked for one tile ahead: K once its scores are formed, V once it is in LDS
+    // (both have to be there when the page after them is known, see above)
     KTile<D> k;
     uint32_t vw[VD];
     constexpr int SW = NG * 64 / 4;                        // dwords of V scales
@@ -784,9 +787,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Args a) {
 // row's maximum and sum. Scores are formed with the rows first (S = Q K^T), so
 // a lane adds four rows of one position by itself and two swaps add the rest; one
 // wave owns a tile, so no atomics. K is read a second time: half the cache's bytes,
-// against writing and reading every row's scores (as much for eight rows a head). 18 us
+// against writing and reading every row's scores (as much for eight rows a head). 19 us
 // for 8 ragged sequences to 16,384 positions of 8 kv heads (45 MB with the weights in
-// and out, 2.5 TB/s), where a form that made q's fragments for every tile took 25 us.
+// and out, 2.4 TB/s), where a form that made q's fragments for every tile took 25 us.
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void attn_weights_kernel(Args a) {
     constexpr int NW = Dim<D>::NW;
@@ -894,9 +897,10 @@ static Launch plan_of(const xp_kv_dims* d, int heads, int q_rows, int batch, int
                                           : waves_per_cu<256, 1>();
     // Contexts of a few rounds are left whole, by as many waves as there is room for. Longer
     // ones are cut into one workgroup of the most waves on each CU where there are few units
-    // (one sequence of 131,072 positions, 4 kv heads: 24 us, against 28 in fours: fewer pieces
-    // to join), else into workgroups of four waves, as many as it holds (8 ragged sequences to
-    // 16,384, 8 kv heads, with weights: 54 us, against 65).
+    // (one sequence of 131,072 positions, 4 kv heads: 25 us, against 29 in fours: fewer pieces
+    // to join), else into workgroups of four waves, as many as it holds (16 ragged sequences to
+    // 8,192, 8 kv heads: 29 us, against 31 in one of twelve; eight to 16,384 with weights 48.5
+    // and 46.6, 48 to 8,192 67 and 64: within 6% either way).
     const bool many = blocks >= 2 * kCus, few = blocks <= 16, cut = tiles > (many ? kLongTiles : 3 * most);
     p.waves = many || (cut && !few) ? 4 : (int)(tiles < most ? tiles : most);
     p.chunk = many ? kLongTiles : 2 * p.waves;

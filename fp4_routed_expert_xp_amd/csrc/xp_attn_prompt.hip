@@ -13,13 +13,15 @@
 //
 // Waves of 32 rows read k and v from LDS half as often; their registers (outputs,
 // scores, q) leave two waves a SIMD up to 128 columns and one at 256, where waves of 16
-// rows leave two: 8 heads of 256 over 4,096 rows take 155 us in those and 233 us in
-// waves of 32, 32 heads of 128 over 8,192 rows 635 us in waves of 16 and 590 us in 32
-// (930 TFLOP/s of the pairs that are seen; a large bf16 product runs at 1,380 here).
+// rows leave two: 8 heads of 256 over 4,096 rows take 158 us in those and took 233 in
+// waves of 32, 32 heads of 128 over 8,192 rows 797 us in waves of 16 and 586 in 32
+// (938 TFLOP/s of the pairs that are seen; a large bf16 product runs at 1,380 here).
 // Bound there by both pipes in turn: of the SIMDs' time the matrix pipe is busy 42%,
-// the vector pipe 38% (the exponentials two fifths of it), both at once 10%; the rest
-// is waiting at the barrier of each tile and for LDS. LDS itself is busy 21%, without
-// bank conflicts.
+// the vector pipe 39% (the exponentials two fifths of it), both at once 11%. Much of the
+// rest is waiting for the tile ahead: it is asked for at the top of a tile, but the wait
+// that the compiler puts before the tile's first read of K, whose loads to LDS it cannot
+// tell from the ones just begun, is for all loads in flight. LDS itself is busy 21%,
+// without bank conflicts.
 //
 // Scores, maxima, sums and outputs are fp32; exponentials round once to the type of
 // v (the product's operand; in fp16 as 2^13 times the weight, so that a long tail of
@@ -41,8 +43,8 @@ typedef __attribute__((address_space(1))) const void* gptr;
 constexpr int kPos = 64;     // positions of a tile
 // Up to this many workgroups of 128 rows (two for each CU) they are of 64 rows, in waves
 // of 16: each CU's chain of tiles is shorter. 2,000 rows of 16/8 heads of 128 (264
-// workgroups) take 48 us so and 58 us in 128 rows, 1,000 of 32/8 28 and 33; 2,000 of
-// 32/8 (512) 58 and 60; eight packed prompts to 1,000 (1,190) 83 and 61.
+// workgroups) take 48 us so and 57 us in 128 rows, 1,000 of 32/8 28 and 33; 2,000 of
+// 32/8 (512) 57 and 60; eight packed prompts to 1,000 (1,190) 80 and 61.
 constexpr int kFew = 512;
 // In powers of two: by how much the running maximum may lag behind, and what exponentials are
 // held as times the weight. fp16 has the range for both only together (15), so it lags less:
@@ -306,7 +308,7 @@ __global__ __launch_bounds__(64 * ROWS / RW, 2) void attn_prompt_kernel(Args a) 
 
     const uint16_t* kp = a.k + (long long)k0 * a.k_stride + (long long)head * D;
     const uint16_t* vp = a.v + (long long)k0 * a.v_stride + (long long)head * D;
-    // A tile goes straight from memory to LDS, one tile ahead into the other buffer: the
+    // A tile goes straight from memory to LDS, asked for one tile ahead, into the other buffer: the
     // j-th load of a thread fills LDS chunk j * kThreads + tid, and reads the chunk that the
     // permutation above puts there. Rows behind the last key repeat it (no row sees them).
     const int lp = tid / (D / 8), lc = tid % (D / 8);
@@ -381,7 +383,7 @@ __global__ __launch_bounds__(64 * ROWS / RW, 2) void attn_prompt_kernel(Args a) 
         top = over_q<RW, false>(top);
         // Exponentials are taken from a maximum that lags behind, so what was summed needs no
         // factor but in a row's first tiles. mx is the score as it is. Up to kNear in log2 units
-        // its product with the factor, rounded, is within 2^-17 of the maximum, far below the
+        // its product with the factor, rounded, is within 2^-16 of the maximum, far below the
         // exponentials' own rounding, and one fma does; beyond that the factor multiplies
         // differences only, which is right at any size, and nothing lags.
         if (__builtin_expect((__ballot(top > mx + a.lag) | far) != 0, 0)) {

@@ -403,7 +403,10 @@ int xp_kv_read(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t
  *               and must not overlap them otherwise (XP_ERR_SHAPE).
  * The destination pages are either the source's own, entry for entry (as far as they
  * go), or pages that no source entry names. weights: rows of w_stride >= max_pages *
- * page fp32. lens are taken as between 0 and max_pages * page. */
+ * page fp32. lens are taken as between 0 and max_pages * page.
+ * A kept position without a page moves as zeros: where its new place has one it is from
+ * then on a position like any other, a key and a value of zeros, and is attended.
+ * Positions are places in the cache: after an eviction a window counts the kept ones. */
 int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, uint8_t* cache, const int32_t* table,
                 const int32_t* lens, const float* weights, int64_t w_stride, int32_t keep, int32_t sinks,
                 int32_t recent, int32_t dst_pages, const int32_t* dst_table, int32_t* kept, int32_t* lens_out,
@@ -415,7 +418,13 @@ int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, uint8_
  * A row at position p sees positions <= p of its sequence, with window > 0 only the
  * last `window` of them. A row that sees nothing is 0, and so is one all of whose
  * scores are -infinity. What a row does not see never reaches it, NaN and infinities
- * included. scale is finite and > 0. Statistics and sums are fp32. */
+ * included. scale is finite and > 0. Scores, statistics and sums are fp32; finite scores
+ * of any size give finite outputs where v is finite and the output type reaches. Each
+ * weight is rounded once before it meets v: decode to fp16, prompt to the type of v; fp16
+ * holds weights below 2^-29 (decode) or 2^-27 (prompt) of the row's largest in steps of
+ * 2^-39 or 2^-37 of it.
+ * Unlike those of the expert and FP8 calls a row's bits may depend on the rest of the
+ * call: on the other rows, on the lengths, in decode also on max_len. */
 
 /* Bytes of workspace of an xp_attn_decode call with these arguments (host, pure; 0 on
  * bad ones). It does not grow evenly with them: ask for each call's own values. */
@@ -448,9 +457,9 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
  * Its last query sits at its last key's position, so a prompt's later piece may
  * attend to the earlier pieces' keys; a query before its first key sees nothing.
  * Rows of out from cu_q[batch] on are left as they were. out may be q itself, with the
- * same stride; otherwise its rows must not overlap rows of q, k or v (XP_ERR_SHAPE). Strides of k and v are below
- * 2^24 elements; with g = heads / kv_heads, (rows_q * g / 64, rounded up, + batch) *
- * kv_heads is below 2^23. */
+ * same stride; otherwise its rows must not overlap rows of q, k or v (XP_ERR_SHAPE).
+ * Strides of k and v are below 2^24 elements; with g = heads / kv_heads, (rows_q * g / 64,
+ * rounded up, + batch) * kv_heads is below 2^23. */
 int xp_attn_prompt(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch, int32_t rows_q, int32_t rows_k,
                    int32_t type, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                    int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, float scale, int32_t window, void* out,
