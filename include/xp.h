@@ -419,10 +419,10 @@ int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, uint8_
  * last `window` of them. A row that sees nothing is 0, and so is one all of whose
  * scores are -infinity. What a row does not see never reaches it, NaN and infinities
  * included. scale is finite and > 0. Scores, statistics and sums are fp32; finite scores
- * of any size give finite outputs where v is finite and the output type reaches. Each
- * weight is rounded once before it meets v: decode to fp16, prompt to the type of v; fp16
- * holds weights below 2^-29 (decode) or 2^-27 (prompt) of the row's largest in steps of
- * 2^-39 or 2^-37 of it.
+ * of any size give finite outputs where the sums of v stay finite too (prompt sums up to
+ * 2^8 times bf16 values: beyond 2^110 or so they may not). Each weight is rounded once
+ * before it meets v: decode to fp16, prompt to the type of v; fp16 holds weights below
+ * 2^-29 (decode) or 2^-27 (prompt) of the row's largest in steps of 2^-39 or 2^-37 of it.
  * Unlike those of the expert and FP8 calls a row's bits may depend on the rest of the
  * call: on the other rows, on the lengths, in decode also on max_len. */
 
