@@ -11,4 +11,6 @@ from .xp import (  # noqa: F401
     xp_workspace_bytes, xp_workspace_layout, xp_fp8_pack, xp_fp8_packed_bytes, xp_fp8_rows,
     xp_gateup_rows_act16, xp_down_rows_act16, xp_combine_y16, xp_fp8_rows_f32, kv_dims, xp_kv_bytes, xp_kv_append,
     xp_kv_read, xp_kv_evict, xp_attn_decode_workspace_bytes, xp_attn_decode, xp_attn_prompt,
+    xp_kv_plan, xp_kv_release, xp_kv_blocks_bytes, xp_kv_blocks, xp_attn_chunk_workspace_bytes, xp_attn_chunk,
+    xp_attn_select, xp_attn_sparse_workspace_bytes, xp_attn_sparse,
 )

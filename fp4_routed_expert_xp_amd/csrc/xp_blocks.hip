@@ -1,0 +1,448 @@
+// xp_blocks.hip — summaries of the cache's blocks of 64 positions, and the choice of the
+// blocks that a query row attends to by a cheap score over them.
+//
+// Everything here is whole numbers, so the chosen lists are a function of the inputs
+// alone, whatever the order of sums:
+//  - a cached key is e2m1 (halves, up to 6) times E4M3 (multiples of 2^-9, up to 448): a
+//    whole number of 2^-10, below 2^22; 64 of them add up to less than 2^28;
+//  - a block's summary is that sum by 2^k in whole steps, head_dim signed bytes;
+//  - a row's q is held as signed bytes by head, times a power of two;
+//  - the product of both is below 127 * 127 * 256 < 2^22, exact in the matrix cores' int32
+//    and in fp32, where the powers of two follow.
+#include "xp_kv_dev.h"
+
+namespace xp {
+namespace blocks {
+
+using kv::Geo;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// The summaries' buffer: head_dim bytes of every entry, then a byte k of every entry;
+// entries are [n_pages][kv_heads][page / 64], as the cache's tiles are.
+__host__ __device__ __forceinline__ long long entries_of(const Geo& g) {
+    return (long long)g.n_pages * g.kv_heads * (g.page / kv::kTilePos);
+}
+
+struct Rows {
+    const int32_t* cu;
+    const int32_t* start;
+    const int32_t* table;
+    int batch, rows;
+};
+
+// The sequence of this lane's row, rows of a wave being consecutive from `first` on.
+__device__ __forceinline__ int lane_sequence(const Rows& m, int first) {
+    const int lane = threadIdx.x & 63, row = first + lane;
+    if (m.batch <= 64) {
+        const int end = lane < m.batch ? m.cu[lane + 1] : 0x7fffffff;
+        int n = 0;
+        for (int b = 0; b < m.batch; ++b) n += __builtin_amdgcn_readlane(end, b) <= row;
+        return n;
+    }
+    int lo = kv::sequence_of_row(m.cu, m.batch, first), hi = kv::sequence_of_row(m.cu, m.batch, first + 63);
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (m.cu[mid + 1] > row)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+// One workgroup: 64 rows and a kv head; a wave for each group of 32 values. The rows at a
+// block's last position complete it: most often one of 64 consecutive rows. A wave takes a
+// position a lane (16 bytes of codes and their scale), and halves values and lanes
+// together, so that 32 sums over 64 lanes cost 32 exchanges.
+template <int NG>
+__global__ __launch_bounds__(64 * NG) void blocks_kernel(Geo g, Rows m, const uint8_t* __restrict__ cache,
+                                                         uint8_t* __restrict__ out) {
+    __shared__ uint32_t tops[2][NG];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int first = (int)(blockIdx.x / g.kv_heads) * 64, head = blockIdx.x % g.kv_heads;
+    const int b = lane_sequence(m, first);
+    long long tile = -1;
+    if (first + lane < m.rows && b < m.batch) {
+        const long long at = (long long)m.start[b] + (first + lane - m.cu[b]);
+        if ((at & 63) == 63 && at >= 0 && at < (long long)g.max_pages * g.page) {
+            const int col = (int)at / g.page, id = m.table[(long long)b * g.max_pages + col];
+            if ((unsigned)id < (unsigned)g.n_pages)
+                tile = ((long long)id * g.kv_heads + head) * (g.page / kv::kTilePos) + ((int)at - col * g.page) / kv::kTilePos;
+        }
+    }
+    uint64_t todo = __ballot(tile >= 0);
+    const int tile_lo = (int)tile, tile_hi = (int)(tile >> 32);
+    for (int turn = 0; todo; todo &= todo - 1, turn ^= 1) {
+        const int l = __ffsll((unsigned long long)todo) - 1;
+        const long long entry = (long long)(uint32_t)__builtin_amdgcn_readlane(tile_lo, l) |
+                                (long long)__builtin_amdgcn_readlane(tile_hi, l) << 32;
+        const uint8_t* t = cache + entry * kv::tile_bytes(NG);
+        const uint4 c = *(const uint4*)(t + wave * 1024 + lane * 16);
+        const uint32_t sb = t[kv::k_scale(NG, lane, wave)];
+        // in units of 2^-10; a NaN scale's values count as zeros
+        const float s = (sb & 127u) == 127u ? 0.0f : kv::e4m3_value(sb) * 1024.0f;
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        int v[32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 1);
+            const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 3);
+            v[8 * i] = (int)(p0.x * s);
+            v[8 * i + 1] = (int)(p0.y * s);
+            v[8 * i + 2] = (int)(p1.x * s);
+            v[8 * i + 3] = (int)(p1.y * s);
+            v[8 * i + 4] = (int)(p2.x * s);
+            v[8 * i + 5] = (int)(p2.y * s);
+            v[8 * i + 6] = (int)(p3.x * s);
+            v[8 * i + 7] = (int)(p3.y * s);
+        }
+        // lane bit 4 - j decides which half of the values is kept: lane l ends with value l % 32 of its half of the lanes
+#pragma unroll
+        for (int n = 16; n >= 1; n >>= 1) {
+            const bool up = lane & n;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < n) {
+                    const int give = up ? v[i] : v[i + n], own = up ? v[i + n] : v[i];
+                    v[i] = own + __shfl_xor(give, n);
+                }
+        }
+        const int total = v[0] + __shfl_xor(v[0], 32);
+        const uint32_t mag = (uint32_t)(total < 0 ? -total : total);
+        const uint32_t top = wave_max_u32(mag);
+        if (lane == 0) tops[turn][wave] = top;
+        __syncthreads();
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) most = tops[turn][i] > most ? tops[turn][i] : most;
+        // the smallest k with most <= 127 * 2^k
+        int k = 0;
+        if (most > 127u) {
+            k = 25 - __builtin_clz(most);      // most in [2^(k + 6), 2^(k + 7))
+            k += most > 127u << k;
+        }
+        // whole steps of 2^k, ties to even; below 2^28, so nothing overflows
+        const uint32_t half = k ? (1u << (k - 1)) - 1u + ((mag >> k) & 1u) : 0u;
+        const int code = (int)((mag + half) >> k);
+        if (lane < 32) out[entry * (32 * NG) + wave * 32 + lane] = (uint8_t)(total < 0 ? -code : code);
+        if (lane == 0 && wave == 0) out[entries_of(g) * (32 * NG) + entry] = (uint8_t)k;
+    }
+}
+
+// ------------------------------------------------------------------ selection
+constexpr int kMaxBlocks = 16384;   // of a sequence: their keys are held in LDS
+
+struct Select {
+    Geo g;
+    Rows m;
+    const void* q;
+    long long q_stride;
+    const uint8_t* codes;
+    const uint8_t* exps;
+    int32_t* sel;
+    int group, keep, sinks, recent;
+};
+
+// A score as an unsigned key in the same order; 0 is below all of them.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float max_over_q(float x) {
+    uint32_t u = __float_as_uint(x);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    u = __float_as_uint(x);
+    auto b = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// q of heads h0 .. h0 + 15 of a kv head as the matrix cores' operand: lane (c, p) holds head
+// h0 + c at dims 64 st + 16 p .. + 15. Returns the exponent e of its steps, the smallest with
+// |q| <= 127 * 2^e; a head that is zero, not finite or not there has zeros and kNone.
+constexpr int kNone = -1000;
+template <int D, bool BF16>
+__device__ __forceinline__ int quantise_q(const Select& a, const uint16_t* q, int h0, i32x4 (&code)[D / 64]) {
+    const int lane = threadIdx.x & 63, c = lane & 15, p = lane >> 4;
+    const bool there = h0 + c < a.group;
+    float x[D / 64][16], top = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int st = 0; st < D / 64; ++st) {
+        const uint16_t* from = q + (long long)(there ? h0 + c : 0) * D + 64 * st + 16 * p;
+        const uint4 u0 = *(const uint4*)from, u1 = *(const uint4*)(from + 8);
+        const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (BF16) {
+                x[st][2 * i] = __uint_as_float(w[i] << 16);
+                x[st][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                x[st][2 * i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i] & 0xffff));
+                x[st][2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i] >> 16));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float m = __builtin_fabsf(x[st][i]);
+            odd |= !(m < __builtin_inff());
+            top = fmaxf(top, m);
+        }
+    }
+    top = max_over_q(odd ? __builtin_inff() : top);
+    int e = kNone;
+    if (there && top > 0.0f && top < __builtin_inff()) {
+        e = __builtin_amdgcn_frexp_expf(top) - 7;
+        e += __builtin_amdgcn_frexp_mantf(top) > 127.0f / 128.0f;
+    }
+#pragma unroll
+    for (int st = 0; st < D / 64; ++st)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float y = __builtin_rintf(__builtin_amdgcn_ldexpf(x[st][4 * j + i], e == kNone ? 0 : -e));
+                w |= (e == kNone ? 0u : (uint32_t)(int)y & 255u) << (8 * i);
+            }
+            code[st][j] = (int)w;
+        }
+    return e;
+}
+
+// One workgroup: a row and a kv head. Scores of 16 blocks at a time by the matrix cores
+// (heads as the rows), keys to LDS; the key of the last block kept by counting passes of 8
+// bits; then each wave walks its run of blocks, once to count and once to write.
+template <int D, bool BF16>
+__global__ __launch_bounds__(1024) void select_kernel(Select a) {
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t bins[256];
+    __shared__ int pick[2];
+    __shared__ int n_over[16], n_tie[16];
+    const int tid = threadIdx.x, lane = tid & 63, threads = blockDim.x, waves = threads >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row = (int)(blockIdx.x / a.g.kv_heads), head = blockIdx.x % a.g.kv_heads;
+    const int b = kv::sequence_of_row(a.m.cu, a.m.batch, row);
+    if (b >= a.m.batch) return;                // rows behind the last sequence
+    int32_t* out = a.sel + ((long long)row * a.g.kv_heads + head) * a.keep;
+    const int cap = a.g.max_pages * a.g.page;
+    long long pos = (long long)a.m.start[b] + (row - a.m.cu[b]);
+    pos = pos >= cap ? cap - 1 : pos;
+    const int n = pos < 0 ? 0 : (int)(pos >> 6) + 1;       // blocks up to the row's own
+    const int m = n < a.keep ? n : a.keep;
+    for (int i = m + tid; i < a.keep; i += threads) out[i] = -1;
+    if (n <= a.keep) {
+        for (int i = tid; i < n; i += threads) out[i] = i;
+        return;
+    }
+    const int lo = a.sinks, hi = n - a.recent;
+    int want = a.keep - a.sinks - a.recent;    // of [lo, hi), which holds more than that
+    uint32_t key = 0;
+    if (want > 0) {
+        const uint16_t* q = (const uint16_t*)a.q + (long long)row * a.q_stride + (long long)head * a.group * D;
+        const int32_t* table = a.m.table + (long long)b * a.g.max_pages;
+        const int c = lane & 15, p = lane >> 4, tiles = a.g.page / kv::kTilePos;
+        i32x4 code[D / 64];
+        int e = quantise_q<D, BF16>(a, q, 0, code), top = e;
+        for (int h0 = 16; h0 < a.group; h0 += 16) {
+            i32x4 unused[D / 64];
+            const int other = quantise_q<D, BF16>(a, q, h0, unused);
+            top = other > top ? other : top;
+        }
+#pragma unroll
+        for (int i = 1; i < 16; i <<= 1) {
+            const int other = __shfl_xor(top, i);
+            top = other > top ? other : top;
+        }
+        for (int h0 = 0; h0 < a.group; h0 += 16) {
+            if (h0) e = quantise_q<D, BF16>(a, q, h0, code);
+            // each head's steps against the largest ones', down to 2^-64 of them
+            const float f = __builtin_amdgcn_ldexpf(1.0f, e - top < -64 ? -64 : e - top);
+            float fr[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fr[i] = __shfl(f, 4 * p + i);
+            for (int base = lo + wave * 16; base < hi; base += waves * 16) {
+                const int blk = base + c < hi ? base + c : hi - 1;
+                const int col = blk / tiles, id = table[col];
+                const bool there = (unsigned)id < (unsigned)a.g.n_pages;
+                const long long entry = there ? ((long long)id * a.g.kv_heads + head) * tiles + (blk - col * tiles) : 0;
+                i32x4 acc = i32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int st = 0; st < D / 64; ++st)
+                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(code[st], *(const i32x4*)(a.codes + entry * D + 64 * st + 16 * p), acc, 0, 0, 0);
+                float best = -__builtin_inff();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (h0 + 4 * p + i < a.group) best = fmaxf(best, (float)acc[i] * fr[i]);
+                best = __builtin_amdgcn_ldexpf(max_over_q(best), a.exps[entry]);
+                if (p == 0 && base + c < hi) {
+                    const uint32_t k = there ? key_of(best) : 0u;
+                    keys[base + c] = h0 && keys[base + c] > k ? keys[base + c] : k;
+                }
+            }
+        }
+        __syncthreads();
+        uint32_t known = 0;
+#pragma unroll 1
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = tid; i < 256; i += threads) bins[i] = 0;
+            __syncthreads();
+            for (int i = lo + tid; i < hi; i += threads) {
+                const uint32_t k = keys[i];
+                if ((k & known) == key) atomicAdd(&bins[(k >> shift) & 255u], 1u);
+            }
+            __syncthreads();
+            if (wave == 0) {                   // lane l has bins 255 - 4 l - j: the largest first
+                int own[4], sum = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    own[j] = (int)bins[255 - 4 * lane - j];
+                    sum += own[j];
+                }
+                int above = wave_incl_sum(sum) - sum;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (above < want && above + own[j] >= want) {
+                        pick[0] = 255 - 4 * lane - j;
+                        pick[1] = want - above;
+                    }
+                    above += own[j];
+                }
+            }
+            __syncthreads();
+            key |= (uint32_t)pick[0] << shift;
+            known |= 255u << shift;
+            want = pick[1];
+        }
+    }
+    // want: how many of the blocks that hold exactly `key` are kept, the lowest first
+    const int run = (n + threads - 1) / threads * 64;
+    const int from = wave * run, to = from + run < n ? from + run : n;
+    const bool any = a.keep > a.sinks + a.recent;
+    int over = 0, tie = 0;
+    for (int i0 = from; i0 < to; i0 += 64) {
+        const int i = i0 + lane;
+        const bool in = i < to, held = in && (i < lo || i >= hi), open = any && in && !held;
+        const uint32_t k = open ? keys[i] : 0u;
+        over += __popcll(__ballot(held || (open && k > key)));
+        tie += __popcll(__ballot(open && k == key));
+    }
+    if (lane == 0) {
+        n_over[wave] = over;
+        n_tie[wave] = tie;
+    }
+    __syncthreads();
+    int at = 0, ties = 0;                      // kept blocks and ties before this wave's run
+    for (int j = 0; j < wave; ++j) {
+        const int left = want - ties;
+        at += n_over[j] + (n_tie[j] < left ? n_tie[j] : left);
+        ties = n_tie[j] < left ? ties + n_tie[j] : want;
+    }
+    const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
+    for (int i0 = from; i0 < to; i0 += 64) {
+        const int i = i0 + lane;
+        const bool in = i < to, held = in && (i < lo || i >= hi), open = any && in && !held;
+        const uint32_t k = open ? keys[i] : 0u;
+        const bool is_tie = open && k == key;
+        const uint64_t bt = __ballot(is_tie);
+        const bool yes = held || (open && k > key) || (is_tie && ties + __popcll(bt & below) < want);
+        const uint64_t by = __ballot(yes);
+        if (yes) out[at + __popcll(by & below)] = i;
+        at += __popcll(by);
+        ties += __popcll(bt);
+    }
+}
+
+static int check_rows(const xp_kv_dims* d, int32_t batch, int32_t max_pages, int32_t rows) {
+    const int st = kv::check_geo(d, batch, max_pages);
+    if (st != XP_OK) return st;
+    // a workgroup for each kv head and row: a launch has fewer than 2^32 threads
+    return rows < 0 || (int64_t)rows * d->kv_heads >= (1 << 22) ? XP_ERR_SHAPE : XP_OK;
+}
+
+}  // namespace blocks
+}  // namespace xp
+
+using namespace xp;
+using namespace xp::blocks;
+
+XP_API size_t xp_kv_blocks_bytes(const xp_kv_dims* dims) {
+    if (!dims || !kv::geo_ok(dims)) return 0;
+    return (size_t)entries_of(kv::geo_of(dims, 1)) * (size_t)(dims->head_dim + 1);
+}
+
+XP_API int xp_kv_blocks(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, const int32_t* cu_rows,
+                        const int32_t* start, const int32_t* table, const uint8_t* cache, uint8_t* blocks, void* stream) {
+    const int st = kv::check_geo(dims, batch, max_pages);
+    if (st != XP_OK) return st;
+    if (rows < 0 || ((int64_t)rows + 63) / 64 * dims->kv_heads >= (1 << 23)) return XP_ERR_SHAPE;   // fewer than 2^32 threads
+    if (batch == 0 || rows == 0) return XP_OK;
+    if (!cu_rows || !start || !table || !cache || !blocks) return XP_ERR_NULL;
+    if (!kv::aligned_to(cu_rows, 4) || !kv::aligned_to(start, 4) || !kv::aligned_to(table, 4) || !kv::aligned_to(cache, 16) ||
+        !kv::aligned_to(blocks, 16))
+        return XP_ERR_SHAPE;
+    const Geo g = kv::geo_of(dims, max_pages);
+    const int64_t held = (int64_t)xp_kv_bytes(dims), made = (int64_t)xp_kv_blocks_bytes(dims);
+    if (kv::rows_meet(kv::Rows{cache, 1, held, held}, kv::Rows{blocks, 1, made, made})) return XP_ERR_SHAPE;
+    const Rows m{cu_rows, start, table, batch, rows};
+    hipStream_t s = (hipStream_t)stream;
+    const dim3 grid((unsigned)((rows + 63) / 64 * (int64_t)dims->kv_heads));
+    if (g.groups == 2)
+        hipLaunchKernelGGL(blocks_kernel<2>, grid, dim3(128), 0, s, g, m, cache, blocks);
+    else if (g.groups == 4)
+        hipLaunchKernelGGL(blocks_kernel<4>, grid, dim3(256), 0, s, g, m, cache, blocks);
+    else
+        hipLaunchKernelGGL(blocks_kernel<8>, grid, dim3(512), 0, s, g, m, cache, blocks);
+    return launch_status();
+}
+
+XP_API int xp_attn_select(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t type,
+                          const void* q, int64_t q_stride, const int32_t* cu_rows, const int32_t* start, const int32_t* table,
+                          const uint8_t* blocks, int32_t keep, int32_t sinks, int32_t recent, int32_t* sel, void* stream) {
+    const int st = check_rows(dims, batch, max_pages, rows);
+    if (st != XP_OK) return st;
+    const int64_t most = (int64_t)max_pages * (dims->page / kv::kTilePos);
+    if (heads < 1 || heads > 65535 || heads % dims->kv_heads || (type != XP_BF16 && type != XP_F16) || most > kMaxBlocks ||
+        sinks < 0 || recent < 1 || (int64_t)sinks + recent > keep || keep > kMaxBlocks)
+        return XP_ERR_SHAPE;
+    if (batch == 0 || rows == 0) return XP_OK;
+    if (!q || !cu_rows || !start || !table || !blocks || !sel) return XP_ERR_NULL;
+    const int64_t width = (int64_t)heads * dims->head_dim;
+    if (q_stride < width || q_stride % 8 || !kv::aligned_to(q, 16) || !kv::aligned_to(cu_rows, 4) || !kv::aligned_to(start, 4) ||
+        !kv::aligned_to(table, 4) || !kv::aligned_to(blocks, 16) || !kv::aligned_to(sel, 4))
+        return XP_ERR_SHAPE;
+    const int64_t made = (int64_t)rows * dims->kv_heads * keep * 4;
+    if (kv::rows_meet(kv::Rows{q, rows, 2 * q_stride, 2 * width}, kv::Rows{sel, 1, made, made})) return XP_ERR_SHAPE;
+    Select a{};
+    a.g = kv::geo_of(dims, max_pages);
+    a.m = Rows{cu_rows, start, table, batch, rows};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.codes = blocks;
+    a.exps = blocks + entries_of(a.g) * dims->head_dim;
+    a.sel = sel;
+    a.group = heads / dims->kv_heads;
+    a.keep = keep;
+    a.sinks = sinks;
+    a.recent = recent;
+    hipStream_t s = (hipStream_t)stream;
+    const dim3 grid((unsigned)(rows * dims->kv_heads)), block(most > 1024 ? 1024 : 256);
+    const unsigned lds = (unsigned)most * 4;
+#define XP_SELECT(D_)                                                                       \
+    do {                                                                                    \
+        if (type == XP_BF16)                                                                \
+            hipLaunchKernelGGL((select_kernel<D_, true>), grid, block, lds, s, a);          \
+        else                                                                                \
+            hipLaunchKernelGGL((select_kernel<D_, false>), grid, block, lds, s, a);         \
+    } while (0)
+    if (dims->head_dim == 64)
+        XP_SELECT(64);
+    else if (dims->head_dim == 128)
+        XP_SELECT(128);
+    else
+        XP_SELECT(256);
+#undef XP_SELECT
+    return launch_status();
+}

@@ -57,6 +57,22 @@ __device__ __forceinline__ int first_seen(int at, int window) {
     return window > 0 && at >= window ? at - window + 1 : 0;
 }
 
+// The sequence of packed row `row`: the number of ends cu[1..batch] at or below it (batch
+// for a row behind the last one). A whole wave, the row the same in all lanes; 64 ends a
+// step, so that 65,535 sequences take three.
+__device__ __forceinline__ int sequence_of_row(const int32_t* __restrict__ cu, int batch, int row) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = batch;
+    while (lo < hi) {
+        const int step = (hi - lo + 63) >> 6, at = lo + (lane + 1) * step;
+        const int n = __popcll(__ballot(cu[at < hi ? at : hi] <= row));
+        const int next = lo + (n + 1) * step;
+        lo = n == 64 || lo + n * step > hi ? hi : lo + n * step;
+        hi = next <= hi ? (next - 1 < lo ? lo : next - 1) : hi;
+    }
+    return lo;
+}
+
 __device__ __forceinline__ float e4m3_value(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0); }
 
 // The smallest E4M3FN scale s with 6 s >= amax (amax >= 0), 448 when there is

@@ -26,7 +26,8 @@ EXPORTS = (
     "xp_gateup_rows_act16", "xp_down_rows_act16", "xp_combine_y16", "xp_fp8_rows_f32", "xp_stream_weights",
     "xp_decode_static", "xp_gateup_rows_coded", "xp_fp8_rows_multi",
     "xp_kv_bytes", "xp_kv_append", "xp_kv_read", "xp_kv_evict", "xp_attn_decode_workspace_bytes", "xp_attn_decode",
-    "xp_attn_prompt",
+    "xp_attn_prompt", "xp_kv_plan", "xp_kv_release", "xp_kv_blocks_bytes", "xp_kv_blocks",
+    "xp_attn_chunk_workspace_bytes", "xp_attn_chunk", "xp_attn_select", "xp_attn_sparse_workspace_bytes", "xp_attn_sparse",
 )
 
 
@@ -113,6 +114,19 @@ def lib():
                                      i64, P, sz, P]
         L.xp_attn_prompt.argtypes = [i32, i32, i32, i32, i32, i32, i32, P, i64, P, i64, P, i64, P, P, ctypes.c_float,
                                      i32, P, i64, P]
+        f32 = ctypes.c_float
+        L.xp_kv_plan.argtypes = [KD, i32, i32, i32] + [P] * 12
+        L.xp_kv_release.argtypes = [KD, i32, i32] + [P] * 6
+        L.xp_kv_blocks_bytes.argtypes = [KD]
+        L.xp_kv_blocks_bytes.restype = sz
+        L.xp_kv_blocks.argtypes = [KD, i32, i32, i32, P, P, P, P, P, P]
+        L.xp_attn_chunk_workspace_bytes.argtypes = [KD, i32, i32, i32, i32]
+        L.xp_attn_chunk_workspace_bytes.restype = sz
+        L.xp_attn_chunk.argtypes = [KD, i32, i32, i32, i32, i32, i32, P, i64, f32, i32, P, P, P, P, P, i64, P, sz, P]
+        L.xp_attn_select.argtypes = [KD, i32, i32, i32, i32, i32, P, i64, P, P, P, P, i32, i32, i32, P, P]
+        L.xp_attn_sparse_workspace_bytes.argtypes = [KD, i32, i32, i32]
+        L.xp_attn_sparse_workspace_bytes.restype = sz
+        L.xp_attn_sparse.argtypes = [KD, i32, i32, i32, i32, i32, i32, P, i64, f32, P, P, P, P, P, P, i64, P, sz, P]
         L.xp_set_tiers.argtypes = [P, i32, P, i32]
         L.xp_get_tiers.argtypes = [P, P, P, P]
         L.xp_status_string.argtypes = [ctypes.c_int]
@@ -123,7 +137,8 @@ def lib():
                      "xp_fp8_pack", "xp_fp8_rows", "xp_gateup_rows_act16", "xp_down_rows_act16",
                      "xp_combine_y16", "xp_fp8_rows_f32", "xp_stream_weights", "xp_decode_static",
                      "xp_gateup_rows_coded", "xp_fp8_rows_multi", "xp_kv_append", "xp_kv_read", "xp_kv_evict",
-                     "xp_attn_decode", "xp_attn_prompt"):
+                     "xp_attn_decode", "xp_attn_prompt", "xp_kv_plan", "xp_kv_release", "xp_kv_blocks",
+                     "xp_attn_chunk", "xp_attn_select", "xp_attn_sparse"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
         try:
@@ -609,6 +624,48 @@ def xp_kv_evict(d: xp_kv_dims, cache, table, lens, weights, keep: int, dst_table
              _arg(kept, i32, "kept", batch * d.kv_heads * keep, dev), _arg(lens_out, i32, "lens_out", batch, dev), op, wo))
 
 
+def xp_kv_plan(d: xp_kv_dims, lens, want, table, free_pages, free_count, cu_rows, start, lens_out, row_seq, row_pos,
+               row_slot, stream=None) -> None:
+    """Pages and places for want[b] new tokens of every sequence, up to row_seq's length in all (see xp.h)."""
+    i32, dev = torch.int32, table.get_device() if isinstance(table, torch.Tensor) else -1
+    tp, batch, cols = _table(table, "table", dev)
+    sp = _arg(row_seq, i32, "row_seq", 0, dev)
+    rows = row_seq.numel()
+    _launch(lib().xp_kv_plan, "xp_kv_plan", dev, stream,
+            (ctypes.byref(d), batch, cols, rows, _arg(lens, i32, "lens", batch, dev), _arg(want, i32, "want", batch, dev), tp,
+             _arg(free_pages, i32, "free_pages", d.n_pages, dev), _arg(free_count, i32, "free_count", 1, dev),
+             _arg(cu_rows, i32, "cu_rows", batch + 1, dev), _arg(start, i32, "start", batch, dev),
+             _arg(lens_out, i32, "lens_out", batch, dev), sp, _arg(row_pos, i32, "row_pos", rows, dev),
+             _arg(row_slot, torch.int64, "row_slot", rows, dev)))
+
+
+def xp_kv_release(d: xp_kv_dims, lens, keep, table, free_pages, free_count, stream=None) -> None:
+    """The pages behind keep[b] positions of every sequence go back to the free ones (see xp.h)."""
+    i32, dev = torch.int32, table.get_device() if isinstance(table, torch.Tensor) else -1
+    tp, batch, cols = _table(table, "table", dev)
+    _launch(lib().xp_kv_release, "xp_kv_release", dev, stream,
+            (ctypes.byref(d), batch, cols, _arg(lens, i32, "lens", batch, dev), _arg(keep, i32, "keep", batch, dev), tp,
+             _arg(free_pages, i32, "free_pages", d.n_pages, dev), _arg(free_count, i32, "free_count", 1, dev)))
+
+
+def xp_kv_blocks_bytes(d: xp_kv_dims) -> int:
+    return int(lib().xp_kv_blocks_bytes(ctypes.byref(d)))
+
+
+def _blocks_bytes(d: xp_kv_dims) -> int:
+    return d.n_pages * d.kv_heads * (d.page // 64) * (d.head_dim + 1)
+
+
+def xp_kv_blocks(d: xp_kv_dims, rows: int, cu_rows, start, table, cache, blocks, stream=None) -> None:
+    """Summarise the blocks of 64 positions that the packed rows complete (see xp.h)."""
+    i32, dev = torch.int32, cache.get_device() if isinstance(cache, torch.Tensor) else -1
+    tp, batch, cols = _table(table, "table", dev)
+    _launch(lib().xp_kv_blocks, "xp_kv_blocks", dev, stream,
+            (ctypes.byref(d), batch, cols, int(rows), _arg(cu_rows, i32, "cu_rows", batch + 1, dev),
+             _arg(start, i32, "start", batch, dev), tp, _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev),
+             _arg(blocks, torch.uint8, "blocks", _blocks_bytes(d), dev)))
+
+
 def xp_attn_decode_workspace_bytes(d: xp_kv_dims, heads: int, q_rows: int, batch: int, max_len: int) -> int:
     return int(lib().xp_attn_decode_workspace_bytes(ctypes.byref(d), int(heads), int(q_rows), int(batch),
                                                     int(max_len)))
@@ -628,6 +685,71 @@ def xp_attn_decode(d: xp_kv_dims, q, cache, table, lens, max_len: int, scale: fl
             (ctypes.byref(d), heads, q_rows, batch, cols, int(max_len), ty, qp, qs, scale, int(window),
              _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev), tp, _arg(lens, torch.int32, "lens", batch, dev), op,
              os_, wp, ws, _arg(workspace, torch.uint8, "workspace", 0, dev), workspace.numel()))
+
+
+def xp_attn_chunk_workspace_bytes(d: xp_kv_dims, heads: int, rows: int, batch: int, max_len: int) -> int:
+    return int(lib().xp_attn_chunk_workspace_bytes(ctypes.byref(d), int(heads), int(rows), int(batch), int(max_len)))
+
+
+def _packed(t, name: str, d: xp_kv_dims):
+    """Packed rows of heads: (address, stride, shape)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError("%s must be [rows][heads][head_dim]" % name)
+    shape = (t.shape[0], t.shape[1], d.head_dim)
+    return _rows3(t, t.dtype, name, shape, t.get_device()) + (shape,)
+
+
+def xp_attn_chunk(d: xp_kv_dims, q, cache, table, cu_rows, start, max_len: int, scale: float, out, workspace,
+                  window: int = 0, stream=None) -> None:
+    """Attention of the packed new tokens q [rows][heads][head_dim] over the 4-bit cache (see xp.h)."""
+    ty, dev, i32 = _type(q, "q", _HALVES), q.get_device(), torch.int32
+    tp, batch, cols = _table(table, "table", dev)
+    qp, qs, shape = _packed(q, "q", d)
+    op, os_ = _rows3(out, q.dtype, "out", shape, dev)
+    _launch(lib().xp_attn_chunk, "xp_attn_chunk", dev, stream,
+            (ctypes.byref(d), shape[1], batch, cols, shape[0], int(max_len), ty, qp, qs, scale, int(window),
+             _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev), tp, _arg(cu_rows, i32, "cu_rows", batch + 1, dev),
+             _arg(start, i32, "start", batch, dev), op, os_, _arg(workspace, torch.uint8, "workspace", 0, dev),
+             workspace.numel()))
+
+
+def xp_attn_select(d: xp_kv_dims, q, cu_rows, start, table, blocks, sel, sinks: int = 0, recent: int = 1,
+                   stream=None) -> None:
+    """The blocks that each row of q attends to, into sel [rows][kv_heads][keep] (see xp.h)."""
+    ty, dev, i32 = _type(q, "q", _HALVES), q.get_device(), torch.int32
+    tp, batch, cols = _table(table, "table", dev)
+    qp, qs, shape = _packed(q, "q", d)
+    sp, keep = _sel(sel, shape[0], d, dev)
+    _launch(lib().xp_attn_select, "xp_attn_select", dev, stream,
+            (ctypes.byref(d), shape[1], batch, cols, shape[0], ty, qp, qs, _arg(cu_rows, i32, "cu_rows", batch + 1, dev),
+             _arg(start, i32, "start", batch, dev), tp, _arg(blocks, torch.uint8, "blocks", _blocks_bytes(d), dev), keep,
+             int(sinks), int(recent), sp))
+
+
+def _sel(t, rows: int, d: xp_kv_dims, dev: int):
+    """Lists of blocks int32 [rows][kv_heads][keep]: (address, keep)."""
+    p = _arg(t, torch.int32, "sel", 0, dev)
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != d.kv_heads:
+        raise ValueError("sel must be [%d, %d, keep], got %s" % (rows, d.kv_heads, list(t.shape)))
+    return p, t.shape[2]
+
+
+def xp_attn_sparse_workspace_bytes(d: xp_kv_dims, heads: int, rows: int, keep: int) -> int:
+    return int(lib().xp_attn_sparse_workspace_bytes(ctypes.byref(d), int(heads), int(rows), int(keep)))
+
+
+def xp_attn_sparse(d: xp_kv_dims, q, cache, table, cu_rows, start, sel, scale: float, out, workspace, stream=None) -> None:
+    """Attention of the packed rows q [rows][heads][head_dim] over the blocks that sel lists (see xp.h)."""
+    ty, dev, i32 = _type(q, "q", _HALVES), q.get_device(), torch.int32
+    tp, batch, cols = _table(table, "table", dev)
+    qp, qs, shape = _packed(q, "q", d)
+    sp, keep = _sel(sel, shape[0], d, dev)
+    op, os_ = _rows3(out, q.dtype, "out", shape, dev)
+    _launch(lib().xp_attn_sparse, "xp_attn_sparse", dev, stream,
+            (ctypes.byref(d), shape[1], batch, cols, shape[0], keep, ty, qp, qs, scale,
+             _arg(cache, torch.uint8, "cache", _cache_bytes(d), dev), tp, _arg(cu_rows, i32, "cu_rows", batch + 1, dev),
+             _arg(start, i32, "start", batch, dev), sp, op, os_, _arg(workspace, torch.uint8, "workspace", 0, dev),
+             workspace.numel()))
 
 
 def xp_attn_prompt(q, k, v, cu_q, cu_k, scale: float, out, window: int = 0, stream=None) -> None:

@@ -412,6 +412,52 @@ int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, uint8_
                 int32_t recent, int32_t dst_pages, const int32_t* dst_table, int32_t* kept, int32_t* lens_out,
                 float* weights_out, int64_t wo_stride, void* stream);
 
+/* Page tables and slot maps of a step, from request lengths, on the GPU. Free pages are a
+ * stack: free_pages int32 [n_pages], of which the first free_count[0] (int32 [1], taken as
+ * between 0 and n_pages) are free, the last of those next. Sequence b holds lens[b] positions
+ * and asks for want[b] more; what is not above 0, or would pass max_pages * page, asks for
+ * nothing, and so does a sequence whose length is below 0. Sequences are served in order as
+ * long as all that is asked for so far fits `rows` rows and the free pages; the first that does
+ * not fit and those behind it get nothing.
+ *   table       [batch][max_pages]: entries ceil(lens / page) .. of a served sequence become its
+ *               new pages, taken from the stack one after the other; no other entry changes;
+ *   free_count  less the pages taken;
+ *   cu_rows     int32 [batch + 1]: running number of new rows, from 0: the row map of the calls
+ *               below, with start;
+ *   start       int32 [batch]: lens;   lens_out  int32 [batch]: lens + new rows; may be lens;
+ *   row_seq, row_pos int32 [rows], row_slot int64 [rows]: of every new row its sequence, its
+ *               position, and its place page * (page's positions) + position in the page, counted
+ *               over all pages (-1 where the table's entry is no page); -1 behind the last new row.
+ * What is written overlaps nothing else (XP_ERR_SHAPE), lens_out excepted. rows is at most 2^24. */
+int xp_kv_plan(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, const int32_t* lens,
+               const int32_t* want, int32_t* table, const int32_t* free_pages, int32_t* free_count, int32_t* cu_rows,
+               int32_t* start, int32_t* lens_out, int32_t* row_seq, int32_t* row_pos, int64_t* row_slot, void* stream);
+
+/* Pages back to the stack: of every sequence the entries ceil(keep / page) .. ceil(lens / page) - 1
+ * (keep below 0 is 0, lens beyond the table is its end) go back where they are pages, and become -1.
+ * keep is 0 for a sequence that has ended, its new length after an eviction or for drafted tokens that
+ * were refused. They are put from the last sequence's last page to the first one's first, so that a
+ * plan undone leaves the stack as it was. A page that another entry still names must not go back.
+ * Pages beyond n_pages of the stack (one that was put twice) are dropped. Nothing overlaps (XP_ERR_SHAPE). */
+int xp_kv_release(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, const int32_t* lens, const int32_t* keep,
+                  int32_t* table, int32_t* free_pages, int32_t* free_count, void* stream);
+
+/* Summaries of the cache's blocks: a block is the 64 positions of a tile. Entry
+ * (page * kv_heads + head) * (page / 64) + tile is head_dim signed bytes at entry * head_dim and one
+ * byte k behind all entries' bytes, at entries * head_dim + entry. With S the sum of the block's 64
+ * keys in units of 2^-10 (whole numbers; a group of 32 values with a NaN scale counts as zeros), k is
+ * the smallest with |S| <= 127 * 2^k everywhere and the bytes are S / 2^k, ties to even: the block's
+ * mean key is byte * 2^(k - 16). The buffer is 16-byte aligned and needs no initial value. */
+
+/* Bytes of the buffer (host, pure; 0 on bad dims). */
+size_t xp_kv_blocks_bytes(const xp_kv_dims* dims);
+
+/* Summarise the blocks that the packed rows complete: call it behind xp_kv_append with the same row
+ * map (after an eviction with start 0 and the kept lengths as rows; k and v themselves are not needed).
+ * A block is complete once its last position is written; positions without a page have none. */
+int xp_kv_blocks(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, const int32_t* cu_rows,
+                 const int32_t* start, const int32_t* table, const uint8_t* cache, uint8_t* blocks, void* stream);
+
 /* ------------------------------------------------------------ attention
  * out = softmax(scale * q k^T over the visible positions) v, for heads query heads
  * that share kv_heads key/value heads (head h reads kv head h / (heads / kv_heads)).
@@ -449,6 +495,50 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
                    int32_t max_len, int32_t type, const void* q, int64_t q_stride, float scale, int32_t window,
                    const uint8_t* cache, const int32_t* table, const int32_t* lens, void* out, int64_t out_stride,
                    float* weights, int64_t w_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/* Attention of packed new tokens over the 4-bit cache: pieces of prompts, single tokens, or both.
+ * q, out: [rows][heads][head_dim] bf16 or fp16 (`type`); cu_rows, start as for xp_kv_append, whose
+ * rows are in the cache already: row cu_rows[b] + i sits at position start[b] + i. One below 0 sees
+ * nothing, one beyond the table sees what the table has. Rows of out from cu_rows[batch] on are
+ * left as they were. max_len (host) sizes the launch and the workspace: no start + rows of a
+ * sequence should exceed it, and one that does is computed all the same, only slower. window, scale,
+ * out = q and overlaps as for xp_attn_decode without weights; the precision is the prompt's in fp16,
+ * for both types. workspace: 16-byte aligned, needs no initial value; calls that share it must not
+ * overlap. Results do not depend on the launch's timing. rows * heads / kv_heads is below
+ * 2^31 - 256, and the row blocks (of 64) of all kv heads below 2^23. */
+size_t xp_attn_chunk_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t rows, int32_t batch, int32_t max_len);
+int xp_attn_chunk(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t max_len,
+                  int32_t type, const void* q, int64_t q_stride, float scale, int32_t window, const uint8_t* cache,
+                  const int32_t* table, const int32_t* cu_rows, const int32_t* start, void* out, int64_t out_stride,
+                  void* workspace, size_t ws_bytes, void* stream);
+
+/* Which blocks a row is to attend to, for every row and kv head: sel int32 [rows][kv_heads][keep],
+ * ascending, then -1. A row sees the blocks 0 .. p / 64 of its sequence, p its position (the table's
+ * last one for a row beyond it). Up to `keep` of them are all listed; of more, the first `sinks`, the
+ * last `recent` (its own among them) and between them those of the largest score, equal scores by the
+ * lower block, a block without a page below every score. recent >= 1, sinks + recent <= keep.
+ * Every head's q is rounded to whole steps of a power of two, the smallest with |q| <= 127 of them, ties
+ * to even, and the score is the largest, over the kv head's heads, of q times the block's mean key
+ * (xp_kv_blocks); a head with an infinity or NaN scores 0, and steps below 2^-64 of the largest head's
+ * count as that. Scores are exact: a row's list depends on its own q and its sequence alone.
+ * The summaries of all blocks before the row's own are in `blocks`. Rows of sel from cu_rows[batch] on
+ * and rows of a position below 0: left as they were, and all -1. max_pages * page / 64 and keep are at
+ * most 16,384, rows * kv_heads below 2^22. sel must not overlap q (XP_ERR_SHAPE). */
+int xp_attn_select(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t type,
+                   const void* q, int64_t q_stride, const int32_t* cu_rows, const int32_t* start, const int32_t* table,
+                   const uint8_t* blocks, int32_t keep, int32_t sinks, int32_t recent, int32_t* sel, void* stream);
+
+/* Attention of packed rows over chosen blocks of the 4-bit cache: sel int32 [rows][kv_heads][keep] as
+ * xp_attn_select makes it, or any other: entries that name no block up to the row's own (-1 among
+ * them), or a block without a page, are skipped, and a block that is named twice counts twice. A row
+ * sees the positions up to its own of the blocks of its kv head's list. Everything else as for
+ * xp_attn_chunk, without a window; the precision is decode's. rows * kv_heads times the sixteens of a
+ * kv head's heads, a part of one counted whole, is below 2^24; keep at most 2^24. */
+size_t xp_attn_sparse_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t rows, int32_t keep);
+int xp_attn_sparse(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t keep,
+                   int32_t type, const void* q, int64_t q_stride, float scale, const uint8_t* cache, const int32_t* table,
+                   const int32_t* cu_rows, const int32_t* start, const int32_t* sel, void* out, int64_t out_stride,
+                   void* workspace, size_t ws_bytes, void* stream);
 
 /* Causal attention over packed prompts. q, out: [rows_q][heads][head_dim], k, v:
  * [rows_k][kv_heads][head_dim], all bf16 or all fp16 (`type`); head_dim 64, 128 or
