@@ -51,10 +51,17 @@ __device__ __forceinline__ int lane_sequence(const Rows& m, int first) {
     return lo;
 }
 
+// Lanes on either side of a pair keep a or b, and add the other side's.
+template <int CTRL>
+__device__ __forceinline__ int halve(int a, int b, bool up) {
+    const int give = up ? a : b, own = up ? b : a;
+    return own + __builtin_amdgcn_mov_dpp(give, CTRL, 0xf, 0xf, true);
+}
+
 // One workgroup: 64 rows and a kv head; a wave for each group of 32 values. The rows at a
 // block's last position complete it: most often one of 64 consecutive rows. A wave takes a
 // position a lane (16 bytes of codes and their scale), and halves values and lanes
-// together, so that 32 sums over 64 lanes cost 32 exchanges.
+// together, so that 32 sums over 64 lanes cost 32 exchanges of one instruction.
 template <int NG>
 __global__ __launch_bounds__(64 * NG) void blocks_kernel(Geo g, Rows m, const uint8_t* __restrict__ cache,
                                                          uint8_t* __restrict__ out) {
@@ -97,18 +104,23 @@ __global__ __launch_bounds__(64 * NG) void blocks_kernel(Geo g, Rows m, const ui
             v[8 * i + 6] = (int)(p3.x * s);
             v[8 * i + 7] = (int)(p3.y * s);
         }
-        // lane bit 4 - j decides which half of the values is kept: lane l ends with value l % 32 of its half of the lanes
+        // halves of the lanes swap halves of the values and add: lane l ends with the sum of value l / 2
 #pragma unroll
-        for (int n = 16; n >= 1; n >>= 1) {
-            const bool up = lane & n;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (i < n) {
-                    const int give = up ? v[i] : v[i + n], own = up ? v[i + n] : v[i];
-                    v[i] = own + __shfl_xor(give, n);
-                }
+        for (int i = 0; i < 16; ++i) {
+            const auto x = __builtin_amdgcn_permlane32_swap(v[i], v[i + 16], false, false);
+            v[i] = (int)(x[0] + x[1]);
         }
-        const int total = v[0] + __shfl_xor(v[0], 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const auto x = __builtin_amdgcn_permlane16_swap(v[i], v[i + 8], false, false);
+            v[i] = (int)(x[0] + x[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = halve<0x128>(v[i], v[i + 4], lane & 8);   // row_ror:8
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = halve<0x141>(v[i], v[i + 2], lane & 4);   // row_half_mirror
+        v[0] = halve<0x4e>(v[0], v[1], lane & 2);                                    // quad_perm 2,3,0,1
+        const int total = v[0] + __builtin_amdgcn_mov_dpp(v[0], 0xb1, 0xf, 0xf, true);   // quad_perm 1,0,3,2
         const uint32_t mag = (uint32_t)(total < 0 ? -total : total);
         const uint32_t top = wave_max_u32(mag);
         if (lane == 0) tops[turn][wave] = top;
@@ -125,13 +137,15 @@ __global__ __launch_bounds__(64 * NG) void blocks_kernel(Geo g, Rows m, const ui
         // whole steps of 2^k, ties to even; below 2^28, so nothing overflows
         const uint32_t half = k ? (1u << (k - 1)) - 1u + ((mag >> k) & 1u) : 0u;
         const int code = (int)((mag + half) >> k);
-        if (lane < 32) out[entry * (32 * NG) + wave * 32 + lane] = (uint8_t)(total < 0 ? -code : code);
+        if ((lane & 1) == 0) out[entry * (32 * NG) + wave * 32 + (lane >> 1)] = (uint8_t)(total < 0 ? -code : code);
         if (lane == 0 && wave == 0) out[entries_of(g) * (32 * NG) + entry] = (uint8_t)k;
     }
 }
 
 // ------------------------------------------------------------------ selection
 constexpr int kMaxBlocks = 16384;   // of a sequence: their keys are held in LDS
+constexpr int kShort = 2048;        // up to so many a wave holds in registers
+constexpr int kCus = 256;
 
 struct Select {
     Geo g;
@@ -142,6 +156,7 @@ struct Select {
     const uint8_t* exps;
     int32_t* sel;
     int group, keep, sinks, recent;
+    int together;         // rows of a workgroup
 };
 
 // A score as an unsigned key in the same order; 0 is below all of them.
@@ -159,20 +174,18 @@ __device__ __forceinline__ float max_over_q(float x) {
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-// q of heads h0 .. h0 + 15 of a kv head as the matrix cores' operand: lane (c, p) holds head
-// h0 + c at dims 64 st + 16 p .. + 15. Returns the exponent e of its steps, the smallest with
-// |q| <= 127 * 2^e; a head that is zero, not finite or not there has zeros and kNone.
+// q of 16 heads as the matrix cores' operand: lane (c, p) holds the head at `from` at dims
+// 64 st + 16 p .. + 15. Returns the exponent e of its steps, the smallest with |q| <= 127 * 2^e;
+// a head that is zero, not finite or not there has zeros and kNone.
 constexpr int kNone = -1000;
 template <int D, bool BF16>
-__device__ __forceinline__ int quantise_q(const Select& a, const uint16_t* q, int h0, i32x4 (&code)[D / 64]) {
-    const int lane = threadIdx.x & 63, c = lane & 15, p = lane >> 4;
-    const bool there = h0 + c < a.group;
+__device__ __forceinline__ int quantise_q(const uint16_t* from, bool there, i32x4 (&code)[D / 64]) {
+    const int p = (threadIdx.x & 63) >> 4;
     float x[D / 64][16], top = 0.0f;
     bool odd = false;
 #pragma unroll
     for (int st = 0; st < D / 64; ++st) {
-        const uint16_t* from = q + (long long)(there ? h0 + c : 0) * D + 64 * st + 16 * p;
-        const uint4 u0 = *(const uint4*)from, u1 = *(const uint4*)(from + 8);
+        const uint4 u0 = *(const uint4*)(from + 64 * st + 16 * p), u1 = *(const uint4*)(from + 64 * st + 16 * p + 8);
         const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -212,26 +225,203 @@ __device__ __forceinline__ int quantise_q(const Select& a, const uint16_t* q, in
     return e;
 }
 
-// One workgroup: a row and a kv head. Scores of 16 blocks at a time by the matrix cores
-// (heads as the rows), keys to LDS; the key of the last block kept by counting passes of 8
-// bits; then each wave walks its run of blocks, once to count and once to write.
+// One step's shared part of both kernels below: the keys of the blocks [0, n) of T rows of one
+// sequence and a kv head into keys[T][pitch]. A wave takes 64 blocks: a lane looks up one
+// block's page, four products of 16 blocks by 16 (row, head) pairs follow, and a lane ends with
+// its own block's scores. Blocks without a page get the key 1, below that of any score.
+template <int D, bool BF16, int T>
+__device__ __forceinline__ void score_blocks(const Select& a, int row, int rows, int head, int b, int n, uint32_t* keys, int pitch) {
+    const int lane = threadIdx.x & 63, c = lane & 15, p = lane >> 4, waves = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t* table = a.m.table + (long long)b * a.g.max_pages;
+    const int tiles = a.g.page / kv::kTilePos;
+    // pair c of a sixteen from h0 on: row t and head h; T > 1 takes all heads at once
+    const int t = T > 1 ? c / a.group : 0, h = T > 1 ? c - t * a.group : c;
+    const auto at = [&](int h0) {
+        const bool there = t < rows && h0 + h < a.group && t < T;
+        return there ? (const uint16_t*)a.q + (long long)(row + t) * a.q_stride + ((long long)head * a.group + h0 + h) * D : nullptr;
+    };
+    const uint16_t* any = (const uint16_t*)a.q + (long long)row * a.q_stride + (long long)head * a.group * D;
+    // a lane's block of the wave's next 64, and its page: asked for ahead
+    const auto look = [&](int base) { return table[(base + lane < n ? base + lane : n - 1) / tiles]; };
+    int id = wave * 64 < n ? look(wave * 64) : -1;
+    i32x4 code[D / 64];
+    int e = quantise_q<D, BF16>(at(0) ? at(0) : any, at(0), code), top = e;
+    if (T == 1)
+        for (int h0 = 16; h0 < a.group; h0 += 16) {
+            i32x4 unused[D / 64];
+            const int other = quantise_q<D, BF16>(at(h0) ? at(h0) : any, at(h0), unused);
+            top = other > top ? other : top;
+        }
+    for (int i = 1; i < (T > 1 ? a.group : 16); i <<= 1) {
+        const int other = __shfl_xor(top, i);
+        top = other > top ? other : top;
+    }
+    for (int h0 = 0; h0 < a.group; h0 += 16) {
+        if (h0) e = quantise_q<D, BF16>(at(h0) ? at(h0) : any, at(h0), code);
+        // each head's steps against the largest ones', down to 2^-64 of them
+        const float f = __builtin_amdgcn_ldexpf(1.0f, e - top < -64 ? -64 : e - top);
+        float fr[4];
+        int of[4];                             // whose row the lane's four results are
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            fr[i] = __shfl(f, 4 * p + i);
+            of[i] = T > 1 ? (4 * p + i) / a.group : (h0 + 4 * p + i < a.group ? 0 : -1);
+        }
+        for (int base = wave * 64; base < n; base += waves * 64) {
+            const int blk = base + lane < n ? base + lane : n - 1, col = blk / tiles;
+            const bool there = (unsigned)id < (unsigned)a.g.n_pages;
+            const long long entry = there ? ((long long)id * a.g.kv_heads + head) * tiles + (blk - col * tiles) : 0;
+            const int k = a.exps[entry], next = base + waves * 64;
+            if (next < n || h0 + 16 < a.group) id = look(next < n ? next : wave * 64);
+            i32x4 m[4][D / 64];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const long long from = (long long)(uint32_t)__shfl((int)entry, 16 * u + c) | (long long)__shfl((int)(entry >> 32), 16 * u + c) << 32;
+#pragma unroll
+                for (int st = 0; st < D / 64; ++st) m[u][st] = *(const i32x4*)(a.codes + from * D + 64 * st + 16 * p);
+            }
+            float best[T];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                i32x4 acc = i32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int st = 0; st < D / 64; ++st) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(code[st], m[u][st], acc, 0, 0, 0);
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = (float)acc[i] * fr[i];
+#pragma unroll
+                for (int r = 0; r < T; ++r) {
+                    float most = -__builtin_inff();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) most = fmaxf(most, of[i] == r ? x[i] : -__builtin_inff());
+                    most = max_over_q(most);
+                    best[r] = u == 0 || p == u ? most : best[r];
+                }
+            }
+            if (base + lane < n)
+#pragma unroll
+                for (int r = 0; r < T; ++r) {
+                    if (r >= rows) break;
+                    const uint32_t key = there ? key_of(__builtin_amdgcn_ldexpf(best[r], k)) : 1u;
+                    uint32_t* to = keys + r * pitch + blk;
+                    *to = h0 && *to > key ? *to : key;
+                }
+        }
+    }
+}
+
+// Blocks up to a row's own.
+__device__ __forceinline__ int blocks_of(const Select& a, int row, int b) {
+    const int cap = a.g.max_pages * a.g.page;
+    long long pos = (long long)a.m.start[b] + (row - a.m.cu[b]);
+    pos = pos >= cap ? cap - 1 : pos;
+    return pos < 0 ? 0 : (int)(pos >> 6) + 1;
+}
+
+// A wave lists the blocks of one row from their keys, in registers: the key of the last one
+// kept is the largest T with as many keys at or above it as are kept, found bit by bit; once
+// there are just as many the rest of its bits does not matter.
+template <int KPL>
+__device__ __forceinline__ void list_blocks(const Select& a, const uint32_t* keys, int n, int32_t* out) {
+    const int lane = threadIdx.x & 63, last = n - a.recent;
+    uint32_t k[KPL];
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) {
+        const int i = j * 64 + lane;
+        k[j] = i >= n ? 0u : (i < a.sinks || i >= last ? ~0u : keys[i]);
+    }
+    uint32_t key = 0;
+    int over = 0;                              // keys above `key`; at the end those kept for sure
+    int count = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t t = key | 1u << bit;
+        count = 0;
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) count += __popcll(__ballot(k[j] >= t));
+        if (count >= a.keep) key = t;
+        if (count == a.keep) break;
+    }
+    int ties = 0;                              // of the keys equal to `key`: the lowest blocks
+    if (count != a.keep) {
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) over += __popcll(__ballot(k[j] > key));
+        ties = a.keep - over;
+    } else {
+        ties = a.keep;                         // more than there are: all of them
+    }
+    const uint64_t below = (1ull << lane) - 1;
+    int at = 0;
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) {
+        const uint64_t same = __ballot(k[j] == key);
+        const bool yes = k[j] > key || (k[j] == key && __popcll(same & below) < ties);
+        const uint64_t chosen = __ballot(yes);
+        if (yes) out[at + __popcll(chosen & below)] = j * 64 + lane;
+        at += __popcll(chosen);
+        ties -= __popcll(same);
+        ties = ties < 0 ? 0 : ties;
+    }
+}
+
+// Up to T rows and a kv head a workgroup, up to kShort blocks: scores by all waves, lists by a
+// wave each. Rows of one sequence share the summaries they read and the products' 16 pairs.
+template <int D, int T>
+constexpr int most_waves() {
+    return T > 1 ? 4 : (D == 256 ? 8 : 16);
+}
+template <int D, bool BF16, int T>
+__global__ __launch_bounds__((64 * most_waves<D, T>()), D == 256 ? 2 : 4) void select_kernel(Select a) {
+    extern __shared__ uint32_t keys[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int head = blockIdx.x % a.g.kv_heads, pitch = a.g.max_pages * (a.g.page / kv::kTilePos);
+    int row = (int)(blockIdx.x / a.g.kv_heads) * a.together;
+    const int end = row + a.together < a.m.rows ? row + a.together : a.m.rows;
+    while (row < end) {
+        const int b = kv::sequence_of_row(a.m.cu, a.m.batch, row);
+        if (b >= a.m.batch) return;            // rows behind the last sequence
+        const int stop = a.m.cu[b + 1], next = stop > row && stop < end ? stop : end, rows = next - row;
+        const int most = blocks_of(a, next - 1, b);        // the last row's are the most
+        if (most > a.keep && a.keep > a.sinks + a.recent) score_blocks<D, BF16, T>(a, row, rows, head, b, most, keys, pitch);
+        __syncthreads();
+        if (wave < rows) {
+            const int n = blocks_of(a, row + wave, b);
+            int32_t* out = a.sel + ((long long)(row + wave) * a.g.kv_heads + head) * a.keep;
+            if (n <= a.keep)
+                for (int i = lane; i < a.keep; i += 64) out[i] = i < n ? i : -1;
+            else if (a.keep == a.sinks + a.recent)
+                for (int i = lane; i < a.keep; i += 64) out[i] = i < a.sinks ? i : n - a.keep + i;
+            else if (n <= 256)
+                list_blocks<4>(a, keys + wave * pitch, n, out);
+            else if (n <= 512)
+                list_blocks<8>(a, keys + wave * pitch, n, out);
+            else if (n <= 1024)
+                list_blocks<16>(a, keys + wave * pitch, n, out);
+            else
+                list_blocks<kShort / 64>(a, keys + wave * pitch, n, out);
+        }
+        row = next;
+        __syncthreads();
+    }
+}
+
+// A row and a kv head a workgroup, any number of blocks: the key of the last block kept by
+// counting passes of 8 bits over LDS; then each wave walks its run of blocks, once to count
+// and once to write.
 template <int D, bool BF16>
-__global__ __launch_bounds__(1024) void select_kernel(Select a) {
+__global__ __launch_bounds__(1024) void select_long_kernel(Select a) {
     extern __shared__ uint32_t keys[];
     __shared__ uint32_t bins[256];
     __shared__ int pick[2];
     __shared__ int n_over[16], n_tie[16];
-    const int tid = threadIdx.x, lane = tid & 63, threads = blockDim.x, waves = threads >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, threads = blockDim.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row = (int)(blockIdx.x / a.g.kv_heads), head = blockIdx.x % a.g.kv_heads;
     const int b = kv::sequence_of_row(a.m.cu, a.m.batch, row);
     if (b >= a.m.batch) return;                // rows behind the last sequence
     int32_t* out = a.sel + ((long long)row * a.g.kv_heads + head) * a.keep;
-    const int cap = a.g.max_pages * a.g.page;
-    long long pos = (long long)a.m.start[b] + (row - a.m.cu[b]);
-    pos = pos >= cap ? cap - 1 : pos;
-    const int n = pos < 0 ? 0 : (int)(pos >> 6) + 1;       // blocks up to the row's own
-    const int m = n < a.keep ? n : a.keep;
+    const int n = blocks_of(a, row, b), m = n < a.keep ? n : a.keep;
     for (int i = m + tid; i < a.keep; i += threads) out[i] = -1;
     if (n <= a.keep) {
         for (int i = tid; i < n; i += threads) out[i] = i;
@@ -241,48 +431,7 @@ __global__ __launch_bounds__(1024) void select_kernel(Select a) {
     int want = a.keep - a.sinks - a.recent;    // of [lo, hi), which holds more than that
     uint32_t key = 0;
     if (want > 0) {
-        const uint16_t* q = (const uint16_t*)a.q + (long long)row * a.q_stride + (long long)head * a.group * D;
-        const int32_t* table = a.m.table + (long long)b * a.g.max_pages;
-        const int c = lane & 15, p = lane >> 4, tiles = a.g.page / kv::kTilePos;
-        i32x4 code[D / 64];
-        int e = quantise_q<D, BF16>(a, q, 0, code), top = e;
-        for (int h0 = 16; h0 < a.group; h0 += 16) {
-            i32x4 unused[D / 64];
-            const int other = quantise_q<D, BF16>(a, q, h0, unused);
-            top = other > top ? other : top;
-        }
-#pragma unroll
-        for (int i = 1; i < 16; i <<= 1) {
-            const int other = __shfl_xor(top, i);
-            top = other > top ? other : top;
-        }
-        for (int h0 = 0; h0 < a.group; h0 += 16) {
-            if (h0) e = quantise_q<D, BF16>(a, q, h0, code);
-            // each head's steps against the largest ones', down to 2^-64 of them
-            const float f = __builtin_amdgcn_ldexpf(1.0f, e - top < -64 ? -64 : e - top);
-            float fr[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) fr[i] = __shfl(f, 4 * p + i);
-            for (int base = lo + wave * 16; base < hi; base += waves * 16) {
-                const int blk = base + c < hi ? base + c : hi - 1;
-                const int col = blk / tiles, id = table[col];
-                const bool there = (unsigned)id < (unsigned)a.g.n_pages;
-                const long long entry = there ? ((long long)id * a.g.kv_heads + head) * tiles + (blk - col * tiles) : 0;
-                i32x4 acc = i32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int st = 0; st < D / 64; ++st)
-                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(code[st], *(const i32x4*)(a.codes + entry * D + 64 * st + 16 * p), acc, 0, 0, 0);
-                float best = -__builtin_inff();
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (h0 + 4 * p + i < a.group) best = fmaxf(best, (float)acc[i] * fr[i]);
-                best = __builtin_amdgcn_ldexpf(max_over_q(best), a.exps[entry]);
-                if (p == 0 && base + c < hi) {
-                    const uint32_t k = there ? key_of(best) : 0u;
-                    keys[base + c] = h0 && keys[base + c] > k ? keys[base + c] : k;
-                }
-            }
-        }
+        score_blocks<D, BF16, 1>(a, row, 1, head, b, n, keys, 0);
         __syncthreads();
         uint32_t known = 0;
 #pragma unroll 1
@@ -362,6 +511,28 @@ static int check_rows(const xp_kv_dims* d, int32_t batch, int32_t max_pages, int
     return rows < 0 || (int64_t)rows * d->kv_heads >= (1 << 22) ? XP_ERR_SHAPE : XP_OK;
 }
 
+template <int D, bool BF16>
+static int launch(Select a, int most, hipStream_t s) {
+    const long long pairs = (long long)a.m.rows * a.g.kv_heads;
+    // Rows of a sequence share a workgroup where they are neighbours on average and workgroups
+    // of four fill the card.
+    const bool many = most <= kShort && (a.group == 1 || a.group == 2 || a.group == 4 || a.group == 8) &&
+                      a.m.rows >= 4ll * a.m.batch && pairs >= 4 * 2 * kCus;
+    a.together = !many ? 1 : (a.group == 8 ? 2 : 4);
+    const long long groups = ((long long)a.m.rows + a.together - 1) / a.together * a.g.kv_heads;
+    const int rounds = (most + 63) / 64, top = most > kShort ? 16 : most_waves<D, 1>();   // rounds of a wave's 64 blocks
+    const int waves = many || (groups >= 2 * kCus && most <= kShort) || rounds < 4 ? 4 : (rounds < top ? rounds : top);
+    const dim3 grid((unsigned)groups), block(64 * waves);
+    const unsigned lds = (unsigned)most * 4 * a.together;
+    if (most > kShort)
+        hipLaunchKernelGGL((select_long_kernel<D, BF16>), grid, block, lds, s, a);
+    else if (many)
+        hipLaunchKernelGGL((select_kernel<D, BF16, 4>), grid, block, lds, s, a);
+    else
+        hipLaunchKernelGGL((select_kernel<D, BF16, 1>), grid, block, lds, s, a);
+    return launch_status();
+}
+
 }  // namespace blocks
 }  // namespace xp
 
@@ -428,21 +599,10 @@ XP_API int xp_attn_select(const xp_kv_dims* dims, int32_t heads, int32_t batch, 
     a.sinks = sinks;
     a.recent = recent;
     hipStream_t s = (hipStream_t)stream;
-    const dim3 grid((unsigned)(rows * dims->kv_heads)), block(most > 1024 ? 1024 : 256);
-    const unsigned lds = (unsigned)most * 4;
-#define XP_SELECT(D_)                                                                       \
-    do {                                                                                    \
-        if (type == XP_BF16)                                                                \
-            hipLaunchKernelGGL((select_kernel<D_, true>), grid, block, lds, s, a);          \
-        else                                                                                \
-            hipLaunchKernelGGL((select_kernel<D_, false>), grid, block, lds, s, a);         \
-    } while (0)
-    if (dims->head_dim == 64)
-        XP_SELECT(64);
-    else if (dims->head_dim == 128)
-        XP_SELECT(128);
-    else
-        XP_SELECT(256);
-#undef XP_SELECT
-    return launch_status();
+    const bool bf = type == XP_BF16;
+    switch (dims->head_dim) {
+        case 64: return bf ? launch<64, true>(a, (int)most, s) : launch<64, false>(a, (int)most, s);
+        case 128: return bf ? launch<128, true>(a, (int)most, s) : launch<128, false>(a, (int)most, s);
+        default: return bf ? launch<256, true>(a, (int)most, s) : launch<256, false>(a, (int)most, s);
+    }
 }
