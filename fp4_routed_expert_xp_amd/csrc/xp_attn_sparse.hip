@@ -33,62 +33,10 @@ struct Args {
     int scale_e;
 };
 
-// q of 16 heads as fp16 fragments and their score factors; a head that is not there is 0.
-template <int D, bool BF16>
-__device__ __forceinline__ float load_q(const Args& a, int row, int head, int hb, int c, int q, h16x8 (&qf)[Dim<D>::NW]) {
-    const int h = hb * 16 + c;
-    const uint16_t* p = (const uint16_t*)a.q + (long long)row * a.q_stride + (long long)(head * a.group + (h < a.group ? h : 0)) * D;
-    uint4 v[Dim<D>::NW];
-#pragma unroll
-    for (int w = 0; w < Dim<D>::NW; ++w) v[w] = h < a.group ? *(const uint4*)(p + dims_of<D>(q, w)) : uint4{0, 0, 0, 0};
-    int k = 0;
-    if constexpr (BF16) {
-        uint32_t top = 0;                      // exponent field of the row's largest magnitude
-#pragma unroll
-        for (int w = 0; w < Dim<D>::NW; ++w) {
-            const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = (u[i] >> 7) & 255u, hi = (u[i] >> 23) & 255u;
-                top = lo > top ? lo : top;
-                top = hi > top ? hi : top;
-            }
-        }
-        const int e = (int)max_over_q((float)top);
-        // largest magnitude to [2^14, 2^15); rows with an infinity or NaN are left as they are
-        k = e == 255 ? 0 : 141 - e;
-        k = k > 100 ? 100 : k;
-        const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-#pragma unroll
-        for (int w = 0; w < Dim<D>::NW; ++w) {
-            const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                qf[w][2 * i] = (_Float16)(__uint_as_float(u[i] << 16) * up);
-                qf[w][2 * i + 1] = (_Float16)(__uint_as_float(u[i] & 0xffff0000u) * up);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int w = 0; w < Dim<D>::NW; ++w) qf[w] = __builtin_bit_cast(h16x8, v[w]);
-    }
-    // kept a normal number: a masked -inf times 0, or a score of 0 times infinity, would be NaN
-    return fminf(fmaxf(__builtin_amdgcn_ldexpf(a.scale_m, a.scale_e - k), 0x1p-126f), 0x1p127f);
-}
-
 template <int D>
 constexpr int waves_per_cu() {
     return D == 64 ? 16 : (D == 128 ? 12 : 8);
 }
-template <int D>
-constexpr int region_bytes() {
-    return Dim<D>::kVBytes + Dim<D>::NG * 64;
-}
-template <int D>
-constexpr int join_bytes() {
-    return Dim<D>::NH * 1024 + 128;
-}
-
 template <int D, bool BF16>
 __device__ __forceinline__ void store_out(const Args& a, int row, int head, int hb, int h, int c, int q, f32x4 o, float sum) {
     if (hb * 16 + c >= a.group) return;
@@ -99,7 +47,6 @@ __device__ __forceinline__ void store_out(const Args& a, int row, int head, int 
 
 template <int D, bool BF16>
 __global__ __launch_bounds__((64 * waves_per_cu<D>())) void attn_sparse_kernel(Args a) {
-    constexpr int NW = Dim<D>::NW, NG = Dim<D>::NG, NH = Dim<D>::NH, VD = Dim<D>::VD;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -115,183 +62,48 @@ __global__ __launch_bounds__((64 * waves_per_cu<D>())) void attn_sparse_kernel(A
     const int32_t* list = a.sel + ((long long)row * a.g.kv_heads + head) * a.keep;
     const int end = (piece + 1) * a.each < a.keep ? (piece + 1) * a.each : a.keep;
 
-    h16x8 qf[NW];
-    const float factor = load_q<D, BF16>(a, row, head, hb, c, q, qf);
-    f32x4 o[NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) o[h] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -__builtin_inff(), l = 0.0f;
-    uint8_t* region = lds + wave * region_bytes<D>();
-
-    KTile<D> k;
-    uint32_t vw[VD];
-    constexpr int SW = NG * 64 / 4;            // dwords of V scales
-    uint32_t vs[(SW + 63) / 64];
-    auto load_v = [&](const uint8_t* t) {
-#pragma unroll
-        for (int j = 0; j < VD / 4; ++j) {
-            const uint4 v = *(const uint4*)(t + NG * 1088 + j * 1024 + lane * 16);
-            vw[4 * j] = v.x;
-            vw[4 * j + 1] = v.y;
-            vw[4 * j + 2] = v.z;
-            vw[4 * j + 3] = v.w;
-        }
-#pragma unroll
-        for (int j = 0; j < (SW + 63) / 64; ++j)
-            vs[j] = j * 64 + lane < SW ? *(const uint32_t*)(t + NG * 2112 + (j * 64 + lane) * 4) : 0u;
-    };
-
-    for (int first = piece * a.each + wave; first < end; first += 64 * waves) {
-        // entry first + lane * waves of the list: its block, and its tile's place
-        const int i = first + lane * waves;
-        const int blk = i < end ? list[i] : -1;
-        long long place = 0;
-        bool there = blk >= 0 && blk <= at >> 6;           // at is below the table's end
-        if (there) {
+    const int h0 = hb * 16 + c;                // the lane's head of the group
+    h16x8 qf[Dim<D>::NW];
+    const float factor = row_frags<D, BF16>((const uint16_t*)a.q + (long long)row * a.q_stride + (long long)(head * a.group + h0) * D,
+                                            h0 < a.group, q, a.scale_m, a.scale_e, qf);
+    Running<D> r;
+    r.clear();
+    uint8_t* region = lds + wave * wave_v_bytes<D>();
+    walk_tiles<D>(
+        a.cache, piece * a.each + wave, end, waves,
+        [&](int i, long long& place) {
+            const int blk = list[i];
+            if (blk < 0 || blk > at >> 6) return -1;       // at is below the table's end
             const int col = blk / tiles, id = tr[col];
-            there = (unsigned)id < (unsigned)a.g.n_pages;
-            place = (((long long)id * a.g.kv_heads + head) * tiles + (blk - col * tiles)) * kv::tile_bytes(NG);
-        }
-        uint64_t todo = __ballot(there);
-        if (!todo) continue;
-        const int place_lo = (int)place, place_hi = (int)(place >> 32);
-        auto tile_of = [&](int j) {
-            return a.cache + ((long long)(uint32_t)__builtin_amdgcn_readlane(place_lo, j) |
-                              (long long)__builtin_amdgcn_readlane(place_hi, j) << 32);
-        };
-        int j = __ffsll((unsigned long long)todo) - 1;
-        {
-            const uint8_t* t = tile_of(j);
-            load_k<D>(k, t, c, q);
-            load_v(t);
-        }
-        while (todo) {
-            todo &= todo - 1;
-            const int base = __builtin_amdgcn_readlane(blk, j) << 6;       // the tile's first position
-            const int nj = todo ? __ffsll((unsigned long long)todo) - 1 : j;
-            const uint8_t* nt = tile_of(nj);
-            f32x4 s[4];
-#pragma unroll
-            for (int bl = 0; bl < 4; ++bl) {
-                s[bl] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = 0; w < NW; ++w) s[bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k_frag<D>(k, bl, w), qf[w], s[bl], 0, 0, 0);
-            }
-            if (todo) load_k<D>(k, nt, c, q);
-            if (base + 63 > at) {
-                // the row's own block: what lies behind it is not seen. Its bytes may be anything, a
-                // NaN scale among them, which a zero weight would let through: its scales are 0
+            place = (((long long)id * a.g.kv_heads + head) * tiles + (blk - col * tiles)) * kv::tile_bytes(Dim<D>::NG);
+            return (unsigned)id < (unsigned)a.g.n_pages ? blk : -1;
+        },
+        [&](int base, f32x4 (&s)[4], VTile<D>& v) {
+            if (base + 63 > at) {              // the row's own block: what lies behind it is not seen
 #pragma unroll
                 for (int bl = 0; bl < 4; ++bl)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (base + 16 * bl + 4 * q + e > at) s[bl][e] = -__builtin_inff();
-#pragma unroll
-                for (int u = 0; u < (SW + 63) / 64; ++u) {
-                    const int at_byte = (u * 64 + lane) * 4;   // byte 4x + y of a group: position 16 (x % 4) + 4 (x / 4) + y
-                    const int x = (at_byte & 63) >> 2;
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        if (base + 16 * (x & 3) + 4 * (x >> 2) + y > at) vs[u] &= ~(255u << (8 * y));
-                }
+                clear_v<D>(v, at + 1 - base, lane);
             }
-            // V to LDS; this wave's earlier reads of the region are done (LDS keeps a wave's order)
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int u = 0; u < VD / 4; ++u)
-                *(uint4*)(region + u * 1024 + lane * 16) = uint4{vw[4 * u], vw[4 * u + 1], vw[4 * u + 2], vw[4 * u + 3]};
-#pragma unroll
-            for (int u = 0; u < (SW + 63) / 64; ++u)
-                if (u * 64 + lane < SW) *(uint32_t*)(region + Dim<D>::kVBytes + (u * 64 + lane) * 4) = vs[u];
-            __builtin_amdgcn_wave_barrier();
-            if (todo) load_v(nt);
-
-            float mx = s[0][0];
-#pragma unroll
-            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e >> 2][e & 3]);
-            mx = max_over_q(mx);
-            if (__ballot(mx > m)) {
-                const float nm = fmaxf(mx, m), safe = nm == -__builtin_inff() ? 0.0f : nm;
-                const float alpha = __builtin_amdgcn_exp2f((m - safe) * factor);
-                m = nm;
-                l *= alpha;
-#pragma unroll
-                for (int h = 0; h < NH; ++h) o[h] *= alpha;
-            }
-            const float top = m == -__builtin_inff() ? 0.0f : m;
-            h16x8 p[2];
-            float add = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3] - top, factor, kLift));
-                add += x;
-                p[e >> 3][e & 7] = (_Float16)x;
-            }
-            l += add;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const uint4 sc = *(const uint4*)(region + Dim<D>::kVBytes + g * 64 + q * 16);
-                const uint32_t sd[4] = {sc.x, sc.y, sc.z, sc.w};
-                h16x2 sv[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sv[2 * e] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sd[e], 1.0f, false);
-                    sv[2 * e + 1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sd[e], 1.0f, true);
-                }
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int h = 2 * g + hh, vrow = 16 * (c >> 2) + 4 * q + (c & 3);
-                    const i32x2 vt = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                        (__attribute__((address_space(3))) i32x2*)(region + h * 512 + vrow * 8));
-#pragma unroll
-                    for (int st = 0; st < 2; ++st)
-                        o[h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            decode8((uint32_t)vt[st], sv[4 * st], sv[4 * st + 1], sv[4 * st + 2], sv[4 * st + 3]), p[st], o[h], 0, 0, 0);
-                }
-            }
-            j = nj;
+            return false;                      // all heads see the same
+        },
+        [](int) {}, qf, factor, r, region);
+    join_waves<D>(r, factor, lds, wave, waves, [&](int h, f32x4 o, float m, float l) {
+        if (a.pieces == 1) {
+            store_out<D, BF16>(a, row, head, hb, h, c, q, o, l);
+            return;
         }
-    }
-
-    // join the waves: each leaves its share in LDS, then takes every waves-th column block
-    l = sum_over_q(l);
-    __syncthreads();
-    {
-        f32x4* buf = (f32x4*)(lds + wave * join_bytes<D>());
-        float* ml = (float*)(buf + NH * 64);
-#pragma unroll
-        for (int h = 0; h < NH; ++h) buf[h * 64 + lane] = o[h];
-        if (q == 0) {
-            ml[c] = m;
-            ml[16 + c] = l;
+        const long long slot = blockIdx.x;
+        ((f32x4*)a.part)[(slot * Dim<D>::NH + h) * 64 + lane] = o;
+        if (h == 0 && q == 0) {
+            float* pm = a.part_ml + slot * 48 + c;
+            pm[0] = m;
+            pm[16] = l;
+            pm[32] = factor;
         }
-    }
-    __syncthreads();
-    for (int h = wave; h < NH; h += waves) {
-        float jm = -__builtin_inff(), jl = 0.0f;
-        for (int w = 0; w < waves; ++w) jm = fmaxf(jm, ((const float*)(lds + w * join_bytes<D>() + NH * 1024))[c]);
-        const float safe = jm == -__builtin_inff() ? 0.0f : jm;
-        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int w = 0; w < waves; ++w) {
-            const uint8_t* from = lds + w * join_bytes<D>();
-            const float* ml = (const float*)(from + NH * 1024) + c;
-            const float f = __builtin_amdgcn_exp2f((ml[0] - safe) * factor);
-            jl = __builtin_fmaf(ml[16], f, jl);
-            acc += ((const f32x4*)from)[h * 64 + lane] * f;
-        }
-        if (a.pieces > 1) {
-            const long long slot = blockIdx.x;
-            ((f32x4*)a.part)[(slot * NH + h) * 64 + lane] = acc;
-            if (h == 0 && q == 0) {
-                float* pm = a.part_ml + slot * 48 + c;
-                pm[0] = jm;
-                pm[16] = jl;
-                pm[32] = factor;
-            }
-            continue;
-        }
-        store_out<D, BF16>(a, row, head, hb, h, c, q, acc, jl);
-    }
+    });
 }
 
 // Joins a unit's pieces, in order: a wave takes four columns of 16 heads a lane.
@@ -359,7 +171,7 @@ static int check_sparse(const xp_kv_dims* d, int heads, int batch, int max_pages
 
 template <int D, bool BF16>
 static int launch(const Args& a, const Launch& p, hipStream_t s) {
-    const int per_wave = join_bytes<D>() > region_bytes<D>() ? join_bytes<D>() : region_bytes<D>();
+    const int per_wave = wave_join_bytes<D>() > wave_v_bytes<D>() ? wave_join_bytes<D>() : wave_v_bytes<D>();
     hipLaunchKernelGGL((attn_sparse_kernel<D, BF16>), dim3((unsigned)(p.units * p.pieces)), dim3(64 * p.waves), p.waves * per_wave, s, a);
     if (p.pieces > 1)
         hipLaunchKernelGGL((sparse_join_kernel<D, BF16>), dim3((unsigned)(p.units * Dim<D>::NH)), dim3(64), 0, s, a);
