@@ -221,8 +221,9 @@ def prepare(case, seed):
 
 # ------------------------------------------------------ the framework's calls
 def _space(s, need):
+    """A program asks once for its workspace, and keeps it."""
     if "ws" not in s:
-        s["ws"] = torch.empty(need, dtype=torch.uint8, device="cuda")
+        s["ws"] = torch.empty(need(), dtype=torch.uint8, device="cuda")
     return s["ws"]
 
 
@@ -237,18 +238,20 @@ def _own(s):
         return s["cu"], s["start"], s["lens_out"], s["seq"], s["pos"], s["slot"], s["table"], s["free"], s["count"]
     kd = xp.kv_dims(s["kv"], s["dim"], s["page"], s["pages"])
     if c["op"] == "chunk":
-        ws = _space(s, xp.xp_attn_chunk_workspace_bytes(kd, c["heads"], s["rows"], s["batch"], s["max_len"]))
+        ws = _space(s, lambda: xp.xp_attn_chunk_workspace_bytes(kd, c["heads"], s["rows"], s["batch"], s["max_len"]))
         xp.xp_attn_chunk(kd, s["q"], s["cache"], s["table"], s["cu"], s["start"], s["max_len"], s["scale"], s["out"], ws,
                          window=c["window"])
         return s["out"]
     if c["op"] == "blocks":
         xp.xp_kv_blocks(kd, s["rows"], s["cu"], s["start"], s["table"], s["cache"], s["blocks"])
-        return _summaries(s)
+        if "parts" not in s:
+            s["parts"] = _summaries(s)
+        return s["parts"]
     if c["op"] == "select":
         xp.xp_attn_select(kd, s["q"], s["cu"], s["start"], s["table"], s["blocks"], s["sel"], sinks=c["sinks"],
                           recent=c["recent"])
         return s["sel"]
-    ws = _space(s, xp.xp_attn_sparse_workspace_bytes(kd, c["heads"], s["rows"], c["keep"]))
+    ws = _space(s, lambda: xp.xp_attn_sparse_workspace_bytes(kd, c["heads"], s["rows"], c["keep"]))
     xp.xp_attn_sparse(kd, s["q"], s["cache"], s["table"], s["cu"], s["start"], s["sel"], s["scale"], s["out"], ws)
     return s["out"]
 
