@@ -45,11 +45,12 @@ __device__ __forceinline__ void store_out(const Args& a, int row, int head, int 
     *(uint2*)(y + 16 * h + 4 * q) = to16<BF16>(o * inv);
 }
 
-template <int D, bool BF16>
-__global__ __launch_bounds__((64 * waves_per_cu<D>())) void attn_sparse_kernel(Args a) {
+// ONE: a wave for each unit, which joins nothing; four of those fit a SIMD up to 128 columns.
+template <int D, bool BF16, bool ONE>
+__global__ __launch_bounds__((ONE ? 64 : 64 * waves_per_cu<D>()), (!ONE ? 1 : D == 64 ? 4 : D == 128 ? 3 : 2)) void attn_sparse_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int wave = ONE ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = ONE ? 1 : blockDim.x >> 6;
     // kv heads next to each other, so that the XCDs share out the heads of a row
     const int unit = blockIdx.x / a.pieces, piece = blockIdx.x - unit * a.pieces;
     const int head = unit % a.g.kv_heads, rest = unit / a.g.kv_heads, hb = rest % a.head_blocks, row = rest / a.head_blocks;
@@ -90,6 +91,12 @@ __global__ __launch_bounds__((64 * waves_per_cu<D>())) void attn_sparse_kernel(A
             return false;                      // all heads see the same
         },
         [](int) {}, qf, factor, r, region);
+    if constexpr (ONE) {
+        r.l = sum_over_q(r.l);
+#pragma unroll
+        for (int h = 0; h < Dim<D>::NH; ++h) store_out<D, BF16>(a, row, head, hb, h, c, q, r.o[h], r.l);
+        return;
+    }
     join_waves<D>(r, factor, lds, wave, waves, [&](int h, f32x4 o, float m, float l) {
         if (a.pieces == 1) {
             store_out<D, BF16>(a, row, head, hb, h, c, q, o, l);
@@ -132,6 +139,7 @@ __global__ __launch_bounds__(64) void sparse_join_kernel(Args a) {
 }
 
 constexpr int kCus = 256;
+constexpr int kOneWave = 8 * kCus;
 
 struct Launch {
     long long units;
@@ -143,10 +151,12 @@ static Launch plan_of(const xp_kv_dims* d, int heads, int rows, int keep) {
     p.head_blocks = (heads / d->kv_heads + 15) / 16;
     p.units = (long long)rows * d->kv_heads * p.head_blocks;
     const int most = d->head_dim == 64 ? waves_per_cu<64>() : d->head_dim == 128 ? waves_per_cu<128>() : waves_per_cu<256>();
-    // Units enough for two a CU are whole, by four waves each; fewer take all the waves that
-    // a CU has, and where their lists are long, several CUs.
+    // Units enough for all waves are one's each; enough for two a CU, four waves'; fewer take all the
+    // waves that a CU has, and where their lists are long, several CUs.
     p.pieces = 1;
-    if (p.units >= 2 * kCus) {
+    if (p.units >= kOneWave) {
+        p.waves = 1;
+    } else if (p.units >= 2 * kCus) {
         p.waves = keep < 4 ? keep : 4;
     } else {
         p.waves = keep < most ? keep : most;
@@ -171,8 +181,12 @@ static int check_sparse(const xp_kv_dims* d, int heads, int batch, int max_pages
 
 template <int D, bool BF16>
 static int launch(const Args& a, const Launch& p, hipStream_t s) {
-    const int per_wave = wave_join_bytes<D>() > wave_v_bytes<D>() ? wave_join_bytes<D>() : wave_v_bytes<D>();
-    hipLaunchKernelGGL((attn_sparse_kernel<D, BF16>), dim3((unsigned)(p.units * p.pieces)), dim3(64 * p.waves), p.waves * per_wave, s, a);
+    static_assert(wave_join_bytes<D>() >= wave_v_bytes<D>());
+    const dim3 grid((unsigned)(p.units * p.pieces)), block(64 * p.waves);
+    if (p.waves == 1 && p.pieces == 1)
+        hipLaunchKernelGGL((attn_sparse_kernel<D, BF16, true>), grid, block, wave_v_bytes<D>(), s, a);
+    else
+        hipLaunchKernelGGL((attn_sparse_kernel<D, BF16, false>), grid, block, p.waves * wave_join_bytes<D>(), s, a);
     if (p.pieces > 1)
         hipLaunchKernelGGL((sparse_join_kernel<D, BF16>), dim3((unsigned)(p.units * Dim<D>::NH)), dim3(64), 0, s, a);
     return launch_status();
