@@ -13,7 +13,8 @@ namespace plan {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr int kOwnPages = 4;       // pages that a sequence's own thread moves; longer runs are a wave's
+constexpr int kOwnPages = 4;       // pages that a sequence's own thread moves
+constexpr int kGroup = 16;         // lanes that move a longer run, four entries each at a time
 constexpr int kOneLaunchRows = 4096;   // up to so many rows, and kThreads sequences, the maps are the same workgroup's
 constexpr int kMaxRows = 1 << 24;
 
@@ -117,10 +118,17 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(Step a, int maps) {
             a.cu[b + 1] = end;
             ends[tid] = end;                   // of use where there is one round
         }
-        for (int i = wave; i < n_runs; i += kWaves) {
+        for (int i = tid / kGroup; i < n_runs; i += kThreads / kGroup) {
             const Run u = runs[i];
-            for (int j = lane; j < u.n; j += 64)
-                a.table[(long long)u.b * a.max_pages + u.col + j] = a.free_pages[height - 1 - (u.base + j)];
+            int32_t* t = a.table + (long long)u.b * a.max_pages + u.col;
+            for (int j0 = tid % kGroup; j0 < u.n; j0 += 4 * kGroup) {
+                int id[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) id[k] = j0 + k * kGroup < u.n ? a.free_pages[height - 1 - (u.base + j0 + k * kGroup)] : 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (j0 + k * kGroup < u.n) t[j0 + k * kGroup] = id[k];
+            }
         }
         __syncthreads();
     }
@@ -213,12 +221,15 @@ __global__ __launch_bounds__(kThreads) void release_kernel(Release a) {
             runs[atomicAdd(&n_runs, 1)] = Run{b, col, n, tid};
         }
         __syncthreads();
-        for (int i = wave; i < n_runs; i += kWaves) {
+        for (int i = tid / kGroup; i < n_runs; i += kThreads / kGroup) {
             const Run u = runs[i];
             const int32_t* ut = a.table + (long long)u.b * a.max_pages + u.col;
             int c = 0;
-            for (int j0 = 0; j0 < u.n; j0 += 64) c += __popcll(__ballot(j0 + lane < u.n && is_page(ut[j0 + lane])));
-            if (lane == 0) found[u.base] = c;
+#pragma unroll 4
+            for (int j = tid % kGroup; j < u.n; j += kGroup) c += is_page(ut[j]);
+#pragma unroll
+            for (int k = 1; k < kGroup; k <<= 1) c += __shfl_xor(c, k);
+            if (tid % kGroup == 0) found[u.base] = c;
         }
         __syncthreads();
         if (!own) pages = found[tid];
@@ -244,17 +255,23 @@ __global__ __launch_bounds__(kThreads) void release_kernel(Release a) {
             found[tid] = to > a.n_pages ? a.n_pages : (int)to;   // entries from n_pages on are not kept
         }
         __syncthreads();
-        for (int i = wave; i < n_runs; i += kWaves) {
+        for (int i = tid / kGroup; i < n_runs; i += kThreads / kGroup) {
             const Run u = runs[i];
             int32_t* ut = a.table + (long long)u.b * a.max_pages + u.col;
             long long put = found[u.base];
-            for (int j0 = u.n - 1; j0 >= 0; j0 -= 64) {
-                const int j = j0 - lane, id = j >= 0 ? ut[j] : -1;
-                const uint64_t there = __ballot(is_page(id));
-                const long long mine = put + __popcll(there & ((1ull << lane) - 1));
-                if (is_page(id) && mine < a.n_pages) a.free_pages[mine] = id;
-                if (j >= 0) ut[j] = -1;
-                put += __popcll(there);
+            for (int j0 = u.n - 1 - tid % kGroup; j0 + tid % kGroup >= 0; j0 -= 4 * kGroup) {
+                int id[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) id[k] = j0 - k * kGroup >= 0 ? ut[j0 - k * kGroup] : -1;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // the pages of the group's lanes, this one's place among them
+                    const uint32_t there = (uint32_t)(__ballot(is_page(id[k])) >> (lane & ~(kGroup - 1))) & ((1u << kGroup) - 1);
+                    const long long mine = put + __popc(there & ((1u << (tid % kGroup)) - 1));
+                    if (is_page(id[k]) && mine < a.n_pages) a.free_pages[mine] = id[k];
+                    if (j0 - k * kGroup >= 0) ut[j0 - k * kGroup] = -1;
+                    put += __popc(there);
+                }
             }
         }
         __syncthreads();
