@@ -281,6 +281,18 @@ __device__ __forceinline__ void score_blocks(const Select& a, int row, int rows,
 #pragma unroll
                 for (int st = 0; st < D / 64; ++st) m[u][st] = *(const i32x4*)(a.codes + from * D + 64 * st + 16 * p);
             }
+            if (T > 1 && a.group == 4) {       // a lane's four results are one row's: it keeps those
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    i32x4 acc = i32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int st = 0; st < D / 64; ++st) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(code[st], m[u][st], acc, 0, 0, 0);
+                    const float most = fmaxf(fmaxf((float)acc[0] * fr[0], (float)acc[1] * fr[1]), fmaxf((float)acc[2] * fr[2], (float)acc[3] * fr[3]));
+                    const int at = 16 * u + c, ku = __shfl(there ? k : -1, at);
+                    if (p < rows && base + at < n) keys[p * pitch + base + at] = ku < 0 ? 1u : key_of(__builtin_amdgcn_ldexpf(most, ku));
+                }
+                continue;
+            }
             float best[T];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -325,29 +337,33 @@ __device__ __forceinline__ int blocks_of(const Select& a, int row, int b) {
 template <int KPL>
 __device__ __forceinline__ void list_blocks(const Select& a, const uint32_t* keys, int n, int32_t* out) {
     const int lane = threadIdx.x & 63, last = n - a.recent;
-    uint32_t k[KPL];
+    uint32_t k[KPL], top = 0;                  // top: of those that are not listed anyway
 #pragma unroll
     for (int j = 0; j < KPL; ++j) {
         const int i = j * 64 + lane;
-        k[j] = i >= n ? 0u : (i < a.sinks || i >= last ? ~0u : keys[i]);
+        const bool open = i >= a.sinks && i < last;
+        k[j] = i >= n ? 0u : (open ? keys[i] : ~0u);
+        top = open && k[j] > top ? k[j] : top;
     }
+    top = wave_max_u32(top);
     uint32_t key = 0;
-    int over = 0;                              // keys above `key`; at the end those kept for sure
-    int count = 0;
+    int over = 0, count = 0;                   // keys above `key`; at or above what is tried
 #pragma unroll 1
     for (int bit = 31; bit >= 0; --bit) {
         const uint32_t t = key | 1u << bit;
+        if (t > top) continue;                 // less than are kept: some of them are open
         count = 0;
 #pragma unroll
-        for (int j = 0; j < KPL; ++j) count += __popcll(__ballot(k[j] >= t));
+        for (int j = 0; j < KPL; ++j) count += k[j] >= t;
+        count = __builtin_amdgcn_readlane(wave_incl_sum(count), 63);
         if (count >= a.keep) key = t;
         if (count == a.keep) break;
     }
     int ties = 0;                              // of the keys equal to `key`: the lowest blocks
     if (count != a.keep) {
 #pragma unroll
-        for (int j = 0; j < KPL; ++j) over += __popcll(__ballot(k[j] > key));
-        ties = a.keep - over;
+        for (int j = 0; j < KPL; ++j) over += k[j] > key;
+        ties = a.keep - __builtin_amdgcn_readlane(wave_incl_sum(over), 63);
     } else {
         ties = a.keep;                         // more than there are: all of them
     }
