@@ -381,14 +381,11 @@ __device__ __forceinline__ void list_blocks(const Select& a, const uint32_t* key
     }
 }
 
-// Up to T rows and a kv head a workgroup, up to kShort blocks: scores by all waves, lists by a
-// wave each. Rows of one sequence share the summaries they read and the products' 16 pairs.
-template <int D, int T>
-constexpr int most_waves() {
-    return T > 1 ? 4 : (D == 256 ? 8 : 16);
-}
-template <int D, bool BF16, int T>
-__global__ __launch_bounds__((64 * most_waves<D, T>()), D == 256 ? 2 : 4) void select_kernel(Select a) {
+// Four rows (two of eight heads) and a kv head a workgroup, up to kShort blocks: scores by all
+// waves, lists by a wave each. Rows of one sequence share the summaries they read and the
+// products' 16 pairs.
+template <int D, bool BF16>
+__global__ __launch_bounds__(256, D == 256 ? 2 : 4) void select_kernel(Select a) {
     extern __shared__ uint32_t keys[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = blockIdx.x % a.g.kv_heads, pitch = a.g.max_pages * (a.g.page / kv::kTilePos);
@@ -399,7 +396,7 @@ __global__ __launch_bounds__((64 * most_waves<D, T>()), D == 256 ? 2 : 4) void s
         if (b >= a.m.batch) return;            // rows behind the last sequence
         const int stop = a.m.cu[b + 1], next = stop > row && stop < end ? stop : end, rows = next - row;
         const int most = blocks_of(a, next - 1, b);        // the last row's are the most
-        if (most > a.keep && a.keep > a.sinks + a.recent) score_blocks<D, BF16, T>(a, row, rows, head, b, most, keys, pitch);
+        if (most > a.keep && a.keep > a.sinks + a.recent) score_blocks<D, BF16, 4>(a, row, rows, head, b, most, keys, pitch);
         __syncthreads();
         if (wave < rows) {
             const int n = blocks_of(a, row + wave, b);
@@ -426,7 +423,7 @@ __global__ __launch_bounds__((64 * most_waves<D, T>()), D == 256 ? 2 : 4) void s
 // counting passes of 8 bits over LDS; then each wave walks its run of blocks, once to count
 // and once to write.
 template <int D, bool BF16>
-__global__ __launch_bounds__(1024) void select_long_kernel(Select a) {
+__global__ __launch_bounds__(1024) void select_row_kernel(Select a) {
     extern __shared__ uint32_t keys[];
     __shared__ uint32_t bins[256];
     __shared__ int pick[2];
@@ -530,22 +527,23 @@ static int check_rows(const xp_kv_dims* d, int32_t batch, int32_t max_pages, int
 template <int D, bool BF16>
 static int launch(Select a, int most, hipStream_t s) {
     const long long pairs = (long long)a.m.rows * a.g.kv_heads;
-    // Rows of a sequence share a workgroup where they are neighbours on average and workgroups
-    // of four fill the card.
+    // Rows of a sequence share a workgroup where they are neighbours on average, from two workgroups'
+    // worth for each CU on (8 kv heads, 1,016 blocks: 64 rows 18 us, one by one 20; 128 rows 19 and 27;
+    // 256 rows 22 and 45).
     const bool many = most <= kShort && (a.group == 1 || a.group == 2 || a.group == 4 || a.group == 8) &&
-                      a.m.rows >= 4ll * a.m.batch && pairs >= 4 * 2 * kCus;
+                      a.m.rows >= 4ll * a.m.batch && pairs >= 2 * kCus;
     a.together = !many ? 1 : (a.group == 8 ? 2 : 4);
     const long long groups = ((long long)a.m.rows + a.together - 1) / a.together * a.g.kv_heads;
-    const int rounds = (most + 63) / 64, top = most > kShort ? 16 : most_waves<D, 1>();   // rounds of a wave's 64 blocks
-    const int waves = many || (groups >= 2 * kCus && most <= kShort) || rounds < 4 ? 4 : (rounds < top ? rounds : top);
+    // Waves take 64 blocks at a time: as many as there are such rounds, four where workgroups fill the
+    // card twice (100 rows of 8 kv heads over 940 blocks: 21 us, in fifteen waves 34).
+    const int rounds = (most + 63) / 64;
+    const int waves = many || groups >= 2 * kCus || rounds < 4 ? 4 : (rounds < 16 ? rounds : 16);
     const dim3 grid((unsigned)groups), block(64 * waves);
     const unsigned lds = (unsigned)most * 4 * a.together;
-    if (most > kShort)
-        hipLaunchKernelGGL((select_long_kernel<D, BF16>), grid, block, lds, s, a);
-    else if (many)
-        hipLaunchKernelGGL((select_kernel<D, BF16, 4>), grid, block, lds, s, a);
+    if (many)
+        hipLaunchKernelGGL((select_kernel<D, BF16>), grid, block, lds, s, a);
     else
-        hipLaunchKernelGGL((select_kernel<D, BF16, 1>), grid, block, lds, s, a);
+        hipLaunchKernelGGL((select_row_kernel<D, BF16>), grid, block, lds, s, a);
     return launch_status();
 }
 
