@@ -32,8 +32,13 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 
 constexpr float kLag = 2.0f, kBlockLift = 13.0f, kNear = 256.0f;   // as prompt attention's in fp16
 constexpr int kWaves = 8;          // of a workgroup: two a SIMD, by registers
-// Rows left behind whole blocks: up to so many are taken by sixteens.
-constexpr int kThin = 64;
+// Rows left behind whole blocks: up to kThin of them are taken by sixteens. Eight sequences of 64
+// such rows behind up to 4,000 positions take 33 us as blocks and 39 as sixteens, 64 sequences of 32
+// rows 113 and 96; one of 64 rows behind 30,000 40 and 34. At 256 columns 64 rows take 33 and 44.
+// Where all sixteens have a workgroup each and contexts are up to kBrief tiles, all rows are taken
+// by sixteens: a workgroup's waves then have the tiles at once (100 rows of 16 heads of 64 behind
+// 200 positions: 6.9 us, as blocks 12.8).
+constexpr int kThin = 32, kBrief = 16;
 
 struct Item {
     int b, kind, first;        // sequence; block 0, sixteen 1; first row
@@ -55,6 +60,7 @@ struct Batch {
     float* part_ml[2];    // their maxima, sums and the rows' factors
     Item* cuts;           // [0].b: how many units of a kv head are cut; then those
     int batch, rows, group, window;
+    int thin;             // rows behind whole blocks up to which they are sixteens
     int share;            // workgroups that the batch is shared out to; 0: no unit is cut
     float scale_m;        // scale * log2(e) = scale_m * 2^scale_e
     int scale_e;
@@ -142,8 +148,8 @@ __device__ __forceinline__ Seq seq_of(const Batch& a, int b) {
     s.rows = (int)n * a.group;
     s.blocks = s.rows / ROWS;
     const int rest = s.rows - s.blocks * ROWS;
-    s.blocks += rest > kThin;
-    s.thin = rest > kThin ? 0 : (rest + 15) >> 4;
+    s.blocks += rest > a.thin;
+    s.thin = rest > a.thin ? 0 : (rest + 15) >> 4;
     const Span first = span_of(a, s.start), last = span_of(a, s.start + n - 1);
     s.lo = first.lo >> 6;
     const int hi = (last.hi + 63) >> 6;
@@ -805,18 +811,21 @@ constexpr int kCus = 256;
 
 struct Launch {
     long long units;               // at most
+    int thin;
     int share, cut;                // workgroups of an even share; units that are cut at most
     size_t part[2], ml[2], total;
 };
 static Launch plan_of(const xp_kv_dims* d, int heads, int rows, int batch, int max_len) {
     Launch p{};
     const long long pairs = (long long)rows * (heads / d->kv_heads), each = d->head_dim == 256 ? 128 : 256;
-    // whole blocks, and behind them of every sequence a part of one or up to kThin / 16 sixteens
-    const long long rest = pairs / 16 + batch, most = (long long)batch * (kThin / 16);
-    p.units = (pairs / each + (rest < most ? rest : most)) * d->kv_heads;
     const int tiles = (int)(((long long)max_len + 63) / 64);
+    // whole blocks, and behind them of every sequence a part of one or up to thin / 16 sixteens
+    const long long rest = pairs / 16 + batch;
+    p.thin = tiles <= kBrief && rest * d->kv_heads <= kCus ? (int)each : kThin;
+    const long long most = (long long)batch * (p.thin / 16);
+    p.units = (pairs / each + (rest < most ? rest : most)) * d->kv_heads;
     // Where all rows are sixteens a join pays for longer sequences only.
-    p.share = tiles > (pairs > kThin ? 8 : 32) ? kCus : 0;
+    p.share = tiles > (pairs > p.thin ? 8 : 32) ? kCus : 0;
     p.cut = (int)(p.units < p.share ? p.units : p.share);
     size_t at = p.share ? align256((p.share + 1) * sizeof(Item)) : 0;
     for (int kind = 0; kind < 2; ++kind) {
@@ -901,6 +910,7 @@ XP_API int xp_attn_chunk(const xp_kv_dims* dims, int32_t heads, int32_t batch, i
     a.rows = rows;
     a.group = heads / dims->kv_heads;
     a.window = window;
+    a.thin = p.thin;
     a.share = p.share;
     a.scale_m = (float)__builtin_frexp((double)scale * 1.4426950408889634, &a.scale_e);
     hipStream_t s = (hipStream_t)stream;
