@@ -505,7 +505,8 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
  * out = q and overlaps as for xp_attn_decode without weights; the precision is the prompt's in fp16,
  * for both types. workspace: 16-byte aligned, needs no initial value; calls that share it must not
  * overlap. Results do not depend on the launch's timing. rows * heads / kv_heads is below
- * 2^31 - 256, and the row blocks (of 64) of all kv heads below 2^23. */
+ * 2^31 - 256, and kv_heads times (that by 256, by 128 at head_dim 256, plus twice the batch) below
+ * 2^23 - 1,280. */
 size_t xp_attn_chunk_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t rows, int32_t batch, int32_t max_len);
 int xp_attn_chunk(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t max_len,
                   int32_t type, const void* q, int64_t q_stride, float scale, int32_t window, const uint8_t* cache,
