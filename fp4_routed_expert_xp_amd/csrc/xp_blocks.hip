@@ -58,6 +58,8 @@ __device__ __forceinline__ int halve(int a, int b, bool up) {
     return own + __builtin_amdgcn_mov_dpp(give, CTRL, 0xf, 0xf, true);
 }
 
+// Bound by its chain of three loads for a step (32 sequences of 16 rows: 7 us), and by the reads
+// of complete blocks for prompts (six of up to 8,100 rows: 18 MB in 12 us, in runs of a kilobyte).
 // One workgroup: 64 rows and a kv head; a wave for each group of 32 values. The rows at a
 // block's last position complete it: most often one of 64 consecutive rows. A wave takes a
 // position a lane (16 bytes of codes and their scale), and halves values and lanes
@@ -421,7 +423,8 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void select_kernel(Select a)
 
 // A row and a kv head a workgroup, any number of blocks: the key of the last block kept by
 // counting passes of 8 bits over LDS; then each wave walks its run of blocks, once to count
-// and once to write.
+// and once to write. (One wave that lists a row from registers, as above, takes 12.8 us where
+// this takes 9.2: 30 rows of 8 kv heads over 516 blocks.)
 template <int D, bool BF16>
 __global__ __launch_bounds__(1024) void select_row_kernel(Select a) {
     extern __shared__ uint32_t keys[];
