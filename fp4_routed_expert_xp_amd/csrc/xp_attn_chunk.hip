@@ -21,10 +21,10 @@
 // rows, kv head) is a unit, and units with more tiles than an even share of the whole are cut
 // along their positions, their pieces joined in order by a second launch.
 //
-// What bounds a block: of a tile's 4,530 cycles the matrix cores work 40%, the vector units 45%
-// (exponentials 8.5 cycles an instruction, others 5), LDS 43%, and they overlap little, since the
-// exponentials wait for the scores and the second product for them: 966 TFLOP/s, 2,048 rows of
-// 32 heads of 128 behind 16,384 positions in 600 us. A mixed step of 512 rows and 16 single tokens
+// What bounds a block: of a tile's 4,530 cycles the matrix cores work 42%, the vector units 45%
+// (a wave issues an exponential every 8.5 cycles, others every 5), both at once 14%, since the
+// exponentials wait for the scores and the second product for them: 988 TFLOP/s, 2,048 rows of
+// 32 heads of 128 behind 16,384 positions in 591 us. A mixed step of 512 rows and 16 single tokens
 // behind up to 4,000 positions takes 67 us.
 #include "xp_attn_dev.h"
 

@@ -7,9 +7,10 @@
 // block, its page, and where its tile lies, 64 entries at once, so that no tile waits for a
 // page number. Few units with long lists are cut into pieces, joined by a second launch.
 //
-// Bound by where the tiles come from: a step of 30 rows of 32 heads of 128, 8 kv heads,
+// Bound by the tiles' bytes where they are read once, else by decoding them (vector pipes 66% busy
+// where a kv head has 4 of the products' 16 columns): a step of 30 rows of 32 heads of 128, 8 kv heads,
 // over 32 blocks each takes 19 us, 3.5 TB/s of tiles that are read once; 512 rows of a prompt over
-// 16 blocks each share theirs and take 72 us, 7.8 TB/s out of the caches.
+// 16 blocks each share theirs and take 72 us, 7.9 TB/s out of the caches.
 #include "xp_attn_dev.h"
 
 namespace xp {
