@@ -147,6 +147,7 @@ __global__ __launch_bounds__(64 * NG) void blocks_kernel(Geo g, Rows m, const ui
 // ------------------------------------------------------------------ selection
 constexpr int kMaxBlocks = 16384;   // of a sequence: their keys are held in LDS
 constexpr int kShort = 2048;        // up to so many a wave holds in registers
+constexpr int kSpare = 8;           // lanes more than are kept that end the search for a bound
 constexpr int kCus = 256;
 
 struct Select {
@@ -336,8 +337,15 @@ __device__ __forceinline__ int blocks_of(const Select& a, int row, int b) {
 // A wave lists the blocks of one row from their keys, in registers: the key of the last one
 // kept is the largest T with as many keys at or above it as are kept, found bit by bit; once
 // there are just as many the rest of its bits does not matter.
+// Up to 64 kept, few lanes' largest keys tell which keys are worth it: as many lanes as are kept have
+// one at or above some bound, so the last one kept is not below it. What is at or above it is most often
+// a wave's worth, a key a lane, in `few` (512 rows of 16 blocks of 1,016: 31 us without, 28 with).
+struct Few {
+    uint32_t key;
+    int block;
+};
 template <int KPL>
-__device__ __forceinline__ void list_blocks(const Select& a, const uint32_t* keys, int n, int32_t* out) {
+__device__ __forceinline__ void list_blocks(const Select& a, const uint32_t* keys, int n, int32_t* out, Few* few) {
     const int lane = threadIdx.x & 63, last = n - a.recent;
     uint32_t k[KPL], top = 0;                  // top: of those that are not listed anyway
 #pragma unroll
@@ -348,6 +356,46 @@ __device__ __forceinline__ void list_blocks(const Select& a, const uint32_t* key
         top = open && k[j] > top ? k[j] : top;
     }
     top = wave_max_u32(top);
+    const uint64_t below = (1ull << lane) - 1;
+    if (a.keep <= 64) {
+        uint32_t own = k[0], bound = 0;
+#pragma unroll
+        for (int j = 1; j < KPL; ++j) own = k[j] > own ? k[j] : own;
+#pragma unroll 1
+        for (int bit = 31; bit >= 0; --bit) {
+            const int lanes = __popcll(__ballot(own >= (bound | 1u << bit)));
+            if (lanes < a.keep) continue;
+            bound |= 1u << bit;
+            if (lanes <= a.keep + kSpare) break;
+        }
+        int held = 0;
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) {
+            const uint64_t in = __ballot(k[j] >= bound);
+            const int to = held + __popcll(in & below);
+            if (k[j] >= bound && to < 64) few[to] = Few{k[j], j * 64 + lane};
+            held += __popcll(in);
+        }
+        if (held <= 64) {
+            __builtin_amdgcn_wave_barrier();
+            const Few x = lane < held ? few[lane] : Few{0u, 0};
+            uint32_t key = 0;
+            int count = held;                  // at or above `key`
+#pragma unroll 1
+            for (int bit = 31; bit >= 0 && count != a.keep; --bit) {
+                const int lanes = __popcll(__ballot(x.key >= (key | 1u << bit)));
+                if (lanes < a.keep) continue;
+                key |= 1u << bit;
+                count = lanes;
+            }
+            const uint64_t same = __ballot(x.key == key && lane < held);
+            const int ties = a.keep - __popcll(__ballot(x.key > key));
+            const bool yes = lane < held && (x.key > key || (x.key == key && __popcll(same & below) < ties));
+            const uint64_t chosen = __ballot(yes);
+            if (yes) out[__popcll(chosen & below)] = x.block;
+            return;
+        }
+    }
     uint32_t key = 0;
     int over = 0, count = 0;                   // keys above `key`; at or above what is tried
 #pragma unroll 1
@@ -369,7 +417,6 @@ __device__ __forceinline__ void list_blocks(const Select& a, const uint32_t* key
     } else {
         ties = a.keep;                         // more than there are: all of them
     }
-    const uint64_t below = (1ull << lane) - 1;
     int at = 0;
 #pragma unroll
     for (int j = 0; j < KPL; ++j) {
@@ -391,6 +438,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void select_kernel(Select a)
     extern __shared__ uint32_t keys[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = blockIdx.x % a.g.kv_heads, pitch = a.g.max_pages * (a.g.page / kv::kTilePos);
+    Few* few = (Few*)(keys + a.together * pitch) + 64 * wave;
     int row = (int)(blockIdx.x / a.g.kv_heads) * a.together;
     const int end = row + a.together < a.m.rows ? row + a.together : a.m.rows;
     while (row < end) {
@@ -408,13 +456,13 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void select_kernel(Select a)
             else if (a.keep == a.sinks + a.recent)
                 for (int i = lane; i < a.keep; i += 64) out[i] = i < a.sinks ? i : n - a.keep + i;
             else if (n <= 256)
-                list_blocks<4>(a, keys + wave * pitch, n, out);
+                list_blocks<4>(a, keys + wave * pitch, n, out, few);
             else if (n <= 512)
-                list_blocks<8>(a, keys + wave * pitch, n, out);
+                list_blocks<8>(a, keys + wave * pitch, n, out, few);
             else if (n <= 1024)
-                list_blocks<16>(a, keys + wave * pitch, n, out);
+                list_blocks<16>(a, keys + wave * pitch, n, out, few);
             else
-                list_blocks<kShort / 64>(a, keys + wave * pitch, n, out);
+                list_blocks<kShort / 64>(a, keys + wave * pitch, n, out, few);
         }
         row = next;
         __syncthreads();
@@ -530,19 +578,20 @@ static int check_rows(const xp_kv_dims* d, int32_t batch, int32_t max_pages, int
 template <int D, bool BF16>
 static int launch(Select a, int most, hipStream_t s) {
     const long long pairs = (long long)a.m.rows * a.g.kv_heads;
-    // Rows of a sequence share a workgroup where they are neighbours on average, from two workgroups'
-    // worth for each CU on (8 kv heads, 1,016 blocks: 64 rows 18 us, one by one 20; 128 rows 19 and 27;
-    // 256 rows 22 and 45).
+    // Rows of a sequence share a workgroup where they are neighbours on average and there are more than
+    // one for each CU (8 kv heads, 1,016 blocks: 32 rows 13.9 us, one by one 12.2; 48 rows 13.8 and 21.7;
+    // 128 rows 14 and 24; 512 rows 27 and 68).
     const bool many = most <= kShort && (a.group == 1 || a.group == 2 || a.group == 4 || a.group == 8) &&
-                      a.m.rows >= 4ll * a.m.batch && pairs >= 2 * kCus;
+                      a.m.rows >= 4ll * a.m.batch && pairs > kCus;
     a.together = !many ? 1 : (a.group == 8 ? 2 : 4);
     const long long groups = ((long long)a.m.rows + a.together - 1) / a.together * a.g.kv_heads;
-    // Waves take 64 blocks at a time: as many as there are such rounds, four where workgroups fill the
-    // card twice (100 rows of 8 kv heads over 940 blocks: 21 us, in fifteen waves 34).
-    const int rounds = (most + 63) / 64;
-    const int waves = many || groups >= 2 * kCus || rounds < 4 ? 4 : (rounds < 16 ? rounds : 16);
+    // Waves take 64 blocks at a time: as many as there are such rounds, up to eight beyond a workgroup for
+    // each CU, four from two on (8 kv heads, 940 blocks: 40 rows in fifteen waves 20 us, in eight 15.6, in
+    // four 16.7; 100 rows in fifteen 34, in four 21).
+    const int rounds = (most + 63) / 64, top = groups > kCus ? 8 : 16;
+    const int waves = many || groups >= 2 * kCus || rounds < 4 ? 4 : (rounds < top ? rounds : top);
     const dim3 grid((unsigned)groups), block(64 * waves);
-    const unsigned lds = (unsigned)most * 4 * a.together;
+    const unsigned lds = (unsigned)most * 4 * a.together + (many ? 4 * 64 * sizeof(Few) : 0);
     if (many)
         hipLaunchKernelGGL((select_kernel<D, BF16>), grid, block, lds, s, a);
     else
