@@ -320,3 +320,15 @@ def test_tensors_that_do_not_fit_are_refused():
     torch.cuda.synchronize()
     for n, t in s.all().items():
         assert torch.equal(t, before[n]), n
+
+
+def test_select_over_the_longest_table():
+    rng = np.random.default_rng(16)
+    c = ref.Cache(2, 64, 1024, 90)
+    table = rng.integers(0, 90, (2, 1024)).astype(np.int32)
+    q = some_q(rng, 5, 6, 64, "bf16")
+    check_select(c, table, ends([3, 2]), [2 ** 20 - 2, 1047000], q, random_blocks(rng, c), 500, 1, 2)
+    d = dims_of(c)
+    with pytest.raises(xp.XPError):
+        xp.xp_attn_select(d, q, dev(ends([3, 2])), ints([0, 0]), dev(np.zeros((2, 1025), dtype=np.int32)),
+                          dev(random_blocks(rng, c)), torch.zeros((5, 2, 5), dtype=torch.int32, device="cuda"))
