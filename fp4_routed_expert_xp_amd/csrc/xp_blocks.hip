@@ -579,10 +579,11 @@ template <int D, bool BF16>
 static int launch(Select a, int most, hipStream_t s) {
     const long long pairs = (long long)a.m.rows * a.g.kv_heads;
     // Rows of a sequence share a workgroup where they are neighbours on average and there are more than
-    // one for each CU (8 kv heads, 1,016 blocks: 32 rows 13.9 us, one by one 12.2; 48 rows 13.8 and 21.7;
-    // 128 rows 14 and 24; 512 rows 27 and 68).
+    // three for each CU, or one where blocks are many (8 kv heads; 1,016 blocks: 32 rows 13.9 us, one by
+    // one 12.2; 48 rows 13.8 and 21.7; 512 rows 27 and 68. 313 blocks: 64 rows 10.5 and 10.1, 128 rows 10.7
+    // and 12.4. 47 blocks: 64 rows 8.6 and 7.3, 128 rows 8.7 and 9.0, 256 rows 10.4 and 13.4).
     const bool many = most <= kShort && (a.group == 1 || a.group == 2 || a.group == 4 || a.group == 8) &&
-                      a.m.rows >= 4ll * a.m.batch && pairs > kCus;
+                      a.m.rows >= 4ll * a.m.batch && pairs > (most > 512 ? 1 : 3) * kCus;
     a.together = !many ? 1 : (a.group == 8 ? 2 : 4);
     const long long groups = ((long long)a.m.rows + a.together - 1) / a.together * a.g.kv_heads;
     // Waves take 64 blocks at a time: as many as there are such rounds, up to eight beyond a workgroup for
