@@ -21,7 +21,9 @@ pytestmark = pytest.mark.gpu
     (16, 1, 256, 64, [33, 7], [500, 3], 4, 1, 1), (8, 2, 128, 192, [64], [5000], 9, 0, 2), (8, 4, 128, 64, [80], [900], 3, 1, 2),
     (8, 4, 64, 64, [64], [127000], 5, 1, 1), (8, 8, 256, 64, [65], [-10], 2, 0, 1), (16, 4, 64, 64, [13, 20, 1], [40000, 63, 20000], 7, 2, 2),
     (8, 3, 128, 64, [70], [3000], 8, 1, 2), (8, 4, 64, 64, [70], [140000], 6, 1, 1), (8, 4, 64, 64, [66], [9000], 70, 1, 1),
-    (8, 4, 128, 64, [66], [5000], 64, 0, 1), (8, 1, 64, 64, [130], [4090], 63, 1, 3)])
+    (8, 4, 128, 64, [66], [5000], 64, 0, 1), (8, 1, 64, 64, [130], [4090], 63, 1, 3),
+    (8, 4, 128, 64, [101], [3000], 8, 1, 2), (8, 8, 64, 128, [97, 0, 3], [1000, 5, 200], 6, 0, 1), (16, 1, 256, 64, [43, 7], [500, 3], 4, 1, 1),
+    (8, 2, 128, 192, [100], [5000], 9, 0, 2), (8, 4, 64, 64, [99], [9000], 70, 1, 1), (8, 4, 128, 64, [100], [900], 3, 1, 2)])
 def test_select_of_neighbouring_rows(kv, group, dim, page, counts, start, keep, sinks, recent):
     rng = np.random.default_rng(sum(counts) + dim + keep)
     batch = len(counts)
