@@ -180,6 +180,16 @@ __global__ __launch_bounds__(256) void map_kernel(Step a) {
         put_none(a, r);
 }
 
+// No sequences: no row anywhere, in the arrays that are there.
+__global__ __launch_bounds__(256) void none_kernel(Step a) {
+    const int r = blockIdx.x * 256 + threadIdx.x;
+    if (r == 0 && a.cu) a.cu[0] = 0;
+    if (r >= a.rows) return;
+    if (a.seq) a.seq[r] = -1;
+    if (a.pos) a.pos[r] = -1;
+    if (a.slot) a.slot[r] = -1;
+}
+
 struct Release {
     const int32_t* lens;
     const int32_t* keep;
@@ -294,7 +304,7 @@ struct Span {
 static bool overlap(const Span* s, int n) {
     for (int i = 0; i < n; ++i)
         for (int j = 0; j < i; ++j) {
-            if (!s[i].written && !s[j].written) continue;
+            if (!s[i].p || !s[j].p || (!s[i].written && !s[j].written)) continue;
             const uintptr_t a = (uintptr_t)s[i].p, b = (uintptr_t)s[j].p;
             if (s[i].bytes > 0 && s[j].bytes > 0 && a < b + s[j].bytes && b < a + s[i].bytes) return true;
         }
@@ -313,20 +323,34 @@ XP_API int xp_kv_plan(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, 
     const int st = kv::check_geo(dims, batch, max_pages);
     if (st != XP_OK) return st;
     if (rows < 0 || rows > kMaxRows) return XP_ERR_SHAPE;
-    if (batch == 0) return XP_OK;
+    hipStream_t s = (hipStream_t)stream;
+    const int64_t b4 = 4 * (int64_t)batch, r4 = 4 * (int64_t)rows;
+    if (batch == 0) {
+        const Span spans[] = {{cu_rows, 4, true}, {row_seq, r4, true}, {row_pos, r4, true}, {row_slot, 2 * r4, true}};
+        for (const Span& x : spans)
+            if (!kv::aligned_to(x.p, x.p == row_slot ? 8 : 4)) return XP_ERR_SHAPE;
+        if (overlap(spans, (int)(sizeof(spans) / sizeof(spans[0])))) return XP_ERR_SHAPE;
+        if (!cu_rows && (rows == 0 || (!row_seq && !row_pos && !row_slot))) return XP_OK;
+        Step a{};
+        a.cu = cu_rows;
+        a.seq = row_seq;
+        a.pos = row_pos;
+        a.slot = (long long*)row_slot;
+        a.rows = rows;
+        hipLaunchKernelGGL(none_kernel, dim3(rows ? (unsigned)((rows + 255) / 256) : 1u), dim3(256), 0, s, a);
+        return launch_status();
+    }
     if (!lens || !want || !table || !free_pages || !free_count || !cu_rows || !start || !lens_out ||
         (rows > 0 && (!row_seq || !row_pos || !row_slot)))
         return XP_ERR_NULL;
-    const int64_t b4 = 4 * (int64_t)batch, r4 = 4 * (int64_t)rows;
     const Span spans[] = {{lens, lens == lens_out ? 0 : b4, false}, {want, b4, false}, {table, b4 * max_pages, true},
                           {free_pages, 4 * (int64_t)dims->n_pages, false}, {free_count, 4, true}, {cu_rows, b4 + 4, true},
                           {start, b4, true}, {lens_out, b4, true}, {row_seq, r4, true}, {row_pos, r4, true}, {row_slot, 2 * r4, true}};
-    for (const Span& s : spans)
-        if (!kv::aligned_to(s.p, 4)) return XP_ERR_SHAPE;
+    for (const Span& x : spans)
+        if (!kv::aligned_to(x.p, 4)) return XP_ERR_SHAPE;
     if (!kv::aligned_to(row_slot, 8) || overlap(spans, (int)(sizeof(spans) / sizeof(spans[0])))) return XP_ERR_SHAPE;
     const Step a{lens, want, table, free_pages, free_count, cu_rows, start, lens_out, row_seq, row_pos, (long long*)row_slot,
                  batch, max_pages, dims->page, dims->n_pages, rows};
-    hipStream_t s = (hipStream_t)stream;
     const bool one = batch <= kThreads && rows <= kOneLaunchRows;
     hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, one ? 1 : 0);
     const int rc = launch_status();

@@ -428,7 +428,8 @@ int xp_kv_evict(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, uint8_
  *   row_seq, row_pos int32 [rows], row_slot int64 [rows]: of every new row its sequence, its
  *               position, and its place page * (page's positions) + position in the page, counted
  *               over all pages (-1 where the table's entry is no page); -1 behind the last new row.
- * What is written overlaps nothing else (XP_ERR_SHAPE), lens_out excepted. rows is at most 2^24. */
+ * What is written overlaps nothing else (XP_ERR_SHAPE), lens_out excepted. rows is at most 2^24.
+ * With batch 0 cu_rows[0] is 0 and the maps are -1, as far as they are there (NULL: left out). */
 int xp_kv_plan(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, const int32_t* lens,
                const int32_t* want, int32_t* table, const int32_t* free_pages, int32_t* free_count, int32_t* cu_rows,
                int32_t* start, int32_t* lens_out, int32_t* row_seq, int32_t* row_pos, int64_t* row_slot, void* stream);
