@@ -229,6 +229,9 @@ XP_API int xp_attn_sparse(const xp_kv_dims* dims, int32_t heads, int32_t batch, 
     // a unit's q is read before its heads are written, but every piece reads it
     const kv::Rows qr{q, rows, 2 * q_stride, 2 * width}, yr{out, rows, 2 * out_stride, 2 * width};
     if (!qr.same(yr) && kv::rows_meet(qr, yr)) return XP_ERR_SHAPE;
+    // other units' lists are still read
+    const int64_t lists = (int64_t)rows * dims->kv_heads * keep * 4;
+    if (kv::rows_meet(kv::Rows{sel, 1, lists, lists}, yr)) return XP_ERR_SHAPE;
     if (ws_bytes < p.total) return XP_ERR_WORKSPACE;
     Args a{};
     a.g = kv::geo_of(dims, max_pages);

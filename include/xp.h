@@ -533,8 +533,8 @@ int xp_attn_select(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t
 /* Attention of packed rows over chosen blocks of the 4-bit cache: sel int32 [rows][kv_heads][keep] as
  * xp_attn_select makes it, or any other: entries that name no block up to the row's own (-1 among
  * them), or a block without a page, are skipped, and a block that is named twice counts twice. A row
- * sees the positions up to its own of the blocks of its kv head's list. Everything else as for
- * xp_attn_chunk, without a window; the precision is decode's. rows * kv_heads times the sixteens of a
+ * sees the positions up to its own of the blocks of its kv head's list. Rows of out must not overlap sel
+ * (XP_ERR_SHAPE). Everything else as for xp_attn_chunk, without a window; the precision is decode's. rows * kv_heads times the sixteens of a
  * kv head's heads, a part of one counted whole, is below 2^24; keep at most 2^24. */
 size_t xp_attn_sparse_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t rows, int32_t keep);
 int xp_attn_sparse(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t keep,
