@@ -898,6 +898,12 @@ XP_API int xp_attn_chunk(const xp_kv_dims* dims, int32_t heads, int32_t batch, i
     const kv::Rows qr{q, rows, 2 * q_stride, 2 * width}, yr{out, rows, 2 * out_stride, 2 * width};
     if (!qr.same(yr) && kv::rows_meet(qr, yr)) return XP_ERR_SHAPE;
     const Launch p = plan_of(dims, heads, rows, batch, max_len);
+    // every workgroup forms the table of pieces from cu and start: were these written over, tables would differ
+    // and pieces lie anywhere
+    const kv::Rows read[] = {kv::flat(cache, (int64_t)xp_kv_bytes(dims)), kv::flat(table, 4 * (int64_t)batch * max_pages),
+                             kv::flat(cu_rows, 4 * (int64_t)batch + 4), kv::flat(start, 4 * (int64_t)batch), qr, yr};
+    if (kv::meets_any(yr, read, 4)) return XP_ERR_SHAPE;
+    if (p.share && kv::meets_any(kv::flat(workspace, (int64_t)(ws_bytes < p.total ? ws_bytes : p.total)), read, 6)) return XP_ERR_SHAPE;
     if (ws_bytes < p.total) return XP_ERR_WORKSPACE;
     Batch a{};
     a.g = kv::geo_of(dims, max_pages);

@@ -229,9 +229,12 @@ XP_API int xp_attn_sparse(const xp_kv_dims* dims, int32_t heads, int32_t batch, 
     // a unit's q is read before its heads are written, but every piece reads it
     const kv::Rows qr{q, rows, 2 * q_stride, 2 * width}, yr{out, rows, 2 * out_stride, 2 * width};
     if (!qr.same(yr) && kv::rows_meet(qr, yr)) return XP_ERR_SHAPE;
-    // other units' lists are still read
-    const int64_t lists = (int64_t)rows * dims->kv_heads * keep * 4;
-    if (kv::rows_meet(kv::Rows{sel, 1, lists, lists}, yr)) return XP_ERR_SHAPE;
+    // what other units still read
+    const kv::Rows read[] = {kv::flat(sel, (int64_t)rows * dims->kv_heads * keep * 4), kv::flat(cache, (int64_t)xp_kv_bytes(dims)),
+                             kv::flat(table, 4 * (int64_t)batch * max_pages), kv::flat(cu_rows, 4 * (int64_t)batch + 4),
+                             kv::flat(start, 4 * (int64_t)batch), qr, yr};
+    if (kv::meets_any(yr, read, 5)) return XP_ERR_SHAPE;
+    if (p.pieces > 1 && kv::meets_any(kv::flat(workspace, (int64_t)(ws_bytes < p.total ? ws_bytes : p.total)), read, 7)) return XP_ERR_SHAPE;
     if (ws_bytes < p.total) return XP_ERR_WORKSPACE;
     Args a{};
     a.g = kv::geo_of(dims, max_pages);

@@ -622,8 +622,9 @@ XP_API int xp_kv_blocks(const xp_kv_dims* dims, int32_t batch, int32_t max_pages
         !kv::aligned_to(blocks, 16))
         return XP_ERR_SHAPE;
     const Geo g = kv::geo_of(dims, max_pages);
-    const int64_t held = (int64_t)xp_kv_bytes(dims), made = (int64_t)xp_kv_blocks_bytes(dims);
-    if (kv::rows_meet(kv::Rows{cache, 1, held, held}, kv::Rows{blocks, 1, made, made})) return XP_ERR_SHAPE;
+    const kv::Rows read[] = {kv::flat(cache, (int64_t)xp_kv_bytes(dims)), kv::flat(cu_rows, 4 * (int64_t)batch + 4),
+                             kv::flat(start, 4 * (int64_t)batch), kv::flat(table, 4 * (int64_t)batch * max_pages)};
+    if (kv::meets_any(kv::flat(blocks, (int64_t)xp_kv_blocks_bytes(dims)), read, 4)) return XP_ERR_SHAPE;
     const Rows m{cu_rows, start, table, batch, rows};
     hipStream_t s = (hipStream_t)stream;
     const dim3 grid((unsigned)((rows + 63) / 64 * (int64_t)dims->kv_heads));
@@ -651,8 +652,10 @@ XP_API int xp_attn_select(const xp_kv_dims* dims, int32_t heads, int32_t batch, 
     if (q_stride < width || q_stride % 8 || !kv::aligned_to(q, 16) || !kv::aligned_to(cu_rows, 4) || !kv::aligned_to(start, 4) ||
         !kv::aligned_to(table, 4) || !kv::aligned_to(blocks, 16) || !kv::aligned_to(sel, 4))
         return XP_ERR_SHAPE;
-    const int64_t made = (int64_t)rows * dims->kv_heads * keep * 4;
-    if (kv::rows_meet(kv::Rows{q, rows, 2 * q_stride, 2 * width}, kv::Rows{sel, 1, made, made})) return XP_ERR_SHAPE;
+    const kv::Rows read[] = {kv::Rows{q, rows, 2 * q_stride, 2 * width}, kv::flat(cu_rows, 4 * (int64_t)batch + 4),
+                             kv::flat(start, 4 * (int64_t)batch), kv::flat(table, 4 * (int64_t)batch * max_pages),
+                             kv::flat(blocks, (int64_t)xp_kv_blocks_bytes(dims))};
+    if (kv::meets_any(kv::flat(sel, (int64_t)rows * dims->kv_heads * keep * 4), read, 5)) return XP_ERR_SHAPE;
     Select a{};
     a.g = kv::geo_of(dims, max_pages);
     a.m = Rows{cu_rows, start, table, batch, rows};

@@ -164,6 +164,14 @@ inline bool rows_meet(const Rows& a, const Rows& b) {
     return false;
 }
 
+// All bytes of an array, and whether rows share one with any of n others.
+inline Rows flat(const void* p, int64_t bytes) { return Rows{p, bytes > 0 ? 1 : 0, bytes, bytes}; }
+inline bool meets_any(const Rows& w, const Rows* others, int n) {
+    for (int i = 0; i < n; ++i)
+        if (rows_meet(w, others[i])) return true;
+    return false;
+}
+
 inline bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 }  // namespace kv

@@ -455,7 +455,8 @@ size_t xp_kv_blocks_bytes(const xp_kv_dims* dims);
 
 /* Summarise the blocks that the packed rows complete: call it behind xp_kv_append with the same row
  * map (after an eviction with start 0 and the kept lengths as rows; k and v themselves are not needed).
- * A block is complete once its last position is written; positions without a page have none. */
+ * A block is complete once its last position is written; positions without a page have none. blocks
+ * must not overlap what is read (XP_ERR_SHAPE). */
 int xp_kv_blocks(const xp_kv_dims* dims, int32_t batch, int32_t max_pages, int32_t rows, const int32_t* cu_rows,
                  const int32_t* start, const int32_t* table, const uint8_t* cache, uint8_t* blocks, void* stream);
 
@@ -502,10 +503,11 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
  * rows are in the cache already: row cu_rows[b] + i sits at position start[b] + i. One below 0 sees
  * nothing, one beyond the table sees what the table has. Rows of out from cu_rows[batch] on are
  * left as they were. max_len (host) sizes the launch and the workspace: no start + rows of a
- * sequence should exceed it, and one that does is computed all the same, only slower. window, scale,
- * out = q and overlaps as for xp_attn_decode without weights; the precision is the prompt's in fp16,
+ * sequence should exceed it, and one that does is computed all the same, only slower. window, scale
+ * and out = q as for xp_attn_decode without weights; otherwise neither rows of out nor the workspace
+ * must overlap what is read, or each other (XP_ERR_SHAPE). The precision is the prompt's in fp16,
  * for both types. workspace: 16-byte aligned, needs no initial value; calls that share it must not
- * overlap. Results do not depend on the launch's timing. rows * heads / kv_heads is below
+ * overlap in time. Results do not depend on the launch's timing. rows * heads / kv_heads is below
  * 2^31 - 256, and kv_heads times (that by 256, by 128 at head_dim 256, plus twice the batch) below
  * 2^23 - 1,280. */
 size_t xp_attn_chunk_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t rows, int32_t batch, int32_t max_len);
@@ -525,7 +527,7 @@ int xp_attn_chunk(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t 
  * count as that. Scores are exact: a row's list depends on its own q and its sequence alone.
  * The summaries of all blocks before the row's own are in `blocks`. Rows of sel from cu_rows[batch] on
  * and rows of a position below 0: left as they were, and all -1. max_pages * page / 64 and keep are at
- * most 16,384, rows * kv_heads below 2^22. sel must not overlap q (XP_ERR_SHAPE). */
+ * most 16,384, rows * kv_heads below 2^22. sel must not overlap what is read (XP_ERR_SHAPE). */
 int xp_attn_select(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t type,
                    const void* q, int64_t q_stride, const int32_t* cu_rows, const int32_t* start, const int32_t* table,
                    const uint8_t* blocks, int32_t keep, int32_t sinks, int32_t recent, int32_t* sel, void* stream);
@@ -533,8 +535,8 @@ int xp_attn_select(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t
 /* Attention of packed rows over chosen blocks of the 4-bit cache: sel int32 [rows][kv_heads][keep] as
  * xp_attn_select makes it, or any other: entries that name no block up to the row's own (-1 among
  * them), or a block without a page, are skipped, and a block that is named twice counts twice. A row
- * sees the positions up to its own of the blocks of its kv head's list. Rows of out must not overlap sel
- * (XP_ERR_SHAPE). Everything else as for xp_attn_chunk, without a window; the precision is decode's. rows * kv_heads times the sixteens of a
+ * sees the positions up to its own of the blocks of its kv head's list. Everything else as for
+ * xp_attn_chunk, without a window; the precision is decode's. rows * kv_heads times the sixteens of a
  * kv head's heads, a part of one counted whole, is below 2^24; keep at most 2^24. */
 size_t xp_attn_sparse_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t rows, int32_t keep);
 int xp_attn_sparse(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t keep,

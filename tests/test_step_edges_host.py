@@ -6,7 +6,7 @@ import pytest
 
 from fp4_routed_expert_xp_amd import xp
 
-from test_step_host import PLAN, SPARSE, at, call
+from test_step_host import BLOCKS, CHUNK, PLAN, SELECT, SPARSE, at, call
 
 
 # ---------------------------------------------------------------- empty batch
@@ -33,3 +33,42 @@ def test_chosen_blocks_are_not_written_over():
                             (512, 1024, False), (2048 - 72, 1024, False), (2048 - 68, 1024, True), (2048 + 508, 1024, True)):
         kw = dict(out=ctypes.c_void_p(base), os=os_, sel=ctypes.c_void_p(base + where), bytes=0)
         assert call("xp_attn_sparse", SPARSE, kw) == (xp.XP_ERR_SHAPE if bad else xp.XP_ERR_WORKSPACE), (where, os_)
+
+
+# the bytes of each array that a call reads, from its sizes in test_step_host.py
+READ = {"xp_kv_blocks": (BLOCKS, dict(cu=8, start=4, table=4)),
+        "xp_attn_select": (SELECT, dict(cu=8, start=4, table=16, blocks=2 * 4 * 65)),
+        "xp_attn_chunk": (CHUNK, dict(cu=8, start=4, table=16, cache=2 * 4 * 2 * 2176)),
+        "xp_attn_sparse": (SPARSE, dict(cu=8, start=4, table=16, cache=2 * 4 * 2 * 2176))}
+# and the array that it writes, with its bytes
+WRITTEN = {"xp_kv_blocks": ("blocks", 2 * 4 * 65), "xp_attn_select": ("sel", 3 * 2 * 3 * 4), "xp_attn_chunk": ("out", 3 * 512),
+           "xp_attn_sparse": ("out", 3 * 512)}
+
+
+@pytest.mark.parametrize("name", list(READ))
+def test_what_a_call_reads_is_not_written_over(name):
+    base, read = READ[name]
+    to, wide = WRITTEN[name]
+    where = base[to].value
+    for key, size in read.items():
+        step = 16 if key in ("cache", "blocks") else 4
+        first = size if size % step == 0 else size + step - size % step
+        for off in (0, wide - wide % step - step, step - first):   # the last place that meets it, and the first
+            assert call(name, base, {key: ctypes.c_void_p(where + off)}) == xp.XP_ERR_SHAPE, (key, off)
+        if "ws" in base:                                       # just beside it: on to the workspace, which is too small
+            for off in (wide + (-wide) % step, -first):
+                assert call(name, base, {key: ctypes.c_void_p(where + off), "bytes": 0}) == xp.XP_ERR_WORKSPACE, (key, off)
+
+
+@pytest.mark.parametrize("name,sizes", [("xp_attn_chunk", dict(rows=40, max_len=9000, cols=150)), ("xp_attn_sparse", dict(rows=1, keep=400, cols=150))])
+def test_a_workspace_over_other_arrays_is_refused(name, sizes):
+    base = READ[name][0]
+    where = base["ws"].value
+    d, rows = xp.kv_dims(2, 64, 64, 4), sizes["rows"]
+    need = xp.xp_attn_chunk_workspace_bytes(d, 4, rows, 1, 9000) if "max_len" in sizes else xp.xp_attn_sparse_workspace_bytes(d, 4, rows, 400)
+    assert need > 4096
+    for key in ("q", "out", "cache", "table", "cu", "start") + (("sel",) if "keep" in sizes else ()):
+        for off in (0, (need - 16) // 16 * 16):
+            assert call(name, base, dict(sizes, bytes=need, **{key: ctypes.c_void_p(where + off)})) == xp.XP_ERR_SHAPE, (key, off)
+        assert call(name, base, dict(sizes, bytes=need - 1, **{key: ctypes.c_void_p(where + (need + 15) // 16 * 16)})) == xp.XP_ERR_WORKSPACE, key
+    assert call(name, base, dict(sizes, bytes=need, q=ctypes.c_void_p(where), out=ctypes.c_void_p(where))) == xp.XP_ERR_SHAPE
