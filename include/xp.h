@@ -509,7 +509,10 @@ int xp_attn_decode(const xp_kv_dims* dims, int32_t heads, int32_t q_rows, int32_
  * for both types. workspace: 16-byte aligned, needs no initial value; calls that share it must not
  * overlap in time. Results do not depend on the launch's timing. rows * heads / kv_heads is below
  * 2^31 - 256, and kv_heads times (that by 256, by 128 at head_dim 256, plus twice the batch) below
- * 2^23 - 1,280. */
+ * 2^23 - 1,280.
+ * Bytes of workspace (host, pure; 0 on bad arguments): 16, or one size for each head_dim (37, 73 and 76 MB)
+ * where sequences may be cut. They never fall as rows, batch or max_len grow: the largest step's are
+ * enough for every smaller one. */
 size_t xp_attn_chunk_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t rows, int32_t batch, int32_t max_len);
 int xp_attn_chunk(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t max_len,
                   int32_t type, const void* q, int64_t q_stride, float scale, int32_t window, const uint8_t* cache,
@@ -537,7 +540,10 @@ int xp_attn_select(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t
  * them), or a block without a page, are skipped, and a block that is named twice counts twice. A row
  * sees the positions up to its own of the blocks of its kv head's list. Everything else as for
  * xp_attn_chunk, without a window; the precision is decode's. rows * kv_heads times the sixteens of a
- * kv head's heads, a part of one counted whole, is below 2^24; keep at most 2^24. */
+ * kv head's heads, a part of one counted whole, is below 2^24; keep at most 2^24.
+ * Bytes of workspace (host, pure; 0 on bad arguments): they do not grow evenly, few rows take more than
+ * many. Ask for each call's own values, or hold 1,024 * (16 * head_dim + 48) bytes (2.1 MB at 128), which
+ * are enough for any. */
 size_t xp_attn_sparse_workspace_bytes(const xp_kv_dims* dims, int32_t heads, int32_t rows, int32_t keep);
 int xp_attn_sparse(const xp_kv_dims* dims, int32_t heads, int32_t batch, int32_t max_pages, int32_t rows, int32_t keep,
                    int32_t type, const void* q, int64_t q_stride, float scale, const uint8_t* cache, const int32_t* table,

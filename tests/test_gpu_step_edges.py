@@ -1,12 +1,12 @@
-"""GPU: a serving step's calls at their edges — an empty batch, sequences of more than one round
-of the plan with long runs of pages."""
+"""GPU: a serving step's calls at their edges — an empty batch, one workspace for steps of any size."""
 import numpy as np
 import pytest
 import torch
 
 from fp4_routed_expert_xp_amd import xp
 
-from test_gpu_attn import dev, ints
+import test_gpu_step as base
+from test_gpu_attn import dev, dims_of, ends, filled, ints, on_device
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,24 @@ def test_plan_without_sequences_captured():
         g.replay()
         torch.cuda.synchronize()
         assert cu.tolist() == [0] and seq.tolist() == [-1] * 9 and pos.tolist() == [-1] * 9 and slot.tolist() == [-1] * 9
+
+
+# ---------------------------------------------------------------------- attention
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_one_workspace_for_steps_of_any_size(dim):
+    """Chosen blocks over the size that suits every call, packed tokens over the largest step's: the bits of calls with their own."""
+    rng = np.random.default_rng(dim + 1)
+    kv, group = 2, 4
+    c = filled(rng, kv, dim, 64, 80)
+    d, buf, table = dims_of(c), on_device(c), rng.integers(0, 80, (1, 200)).astype(np.int32)
+    sparse_ws = torch.full((1024 * (16 * dim + 48),), 255, dtype=torch.uint8, device="cuda")
+    chunk_ws = torch.full((xp.xp_attn_chunk_workspace_bytes(d, kv * group, 300, 1, 12800),), 255, dtype=torch.uint8, device="cuda")
+    for rows, keep in ((1, 190), (15, 40), (16, 64), (31, 64), (32, 64), (33, 7), (64, 64), (300, 3)):
+        q, cu, start = base.some_q(rng, rows, kv * group, dim, "bf16"), ends([rows]), [12000]
+        sel = dev(rng.integers(-1, 188, (rows, kv, keep)).astype(np.int32))
+        out = torch.full_like(q, 3.0)
+        xp.xp_attn_sparse(d, q, buf, dev(table), dev(cu), ints(start), sel, 0.09, out, sparse_ws)
+        assert torch.equal(out, base.run_sparse(c, buf, table, cu, start, q, sel, 0.09)), rows
+        out = torch.full_like(q, 3.0)
+        xp.xp_attn_chunk(d, q, buf, dev(table), dev(cu), ints(start), 12000 + rows, 0.09, out, chunk_ws)
+        assert torch.equal(out, base.run_chunk(c, buf, table, cu, start, q, 0.09)), rows

@@ -1,6 +1,7 @@
 """Host side of a serving step's entry points at their edges (no GPU): an empty batch, outputs
 over inputs, workspaces."""
 import ctypes
+import itertools
 
 import pytest
 
@@ -72,3 +73,25 @@ def test_a_workspace_over_other_arrays_is_refused(name, sizes):
             assert call(name, base, dict(sizes, bytes=need, **{key: ctypes.c_void_p(where + off)})) == xp.XP_ERR_SHAPE, (key, off)
         assert call(name, base, dict(sizes, bytes=need - 1, **{key: ctypes.c_void_p(where + (need + 15) // 16 * 16)})) == xp.XP_ERR_WORKSPACE, key
     assert call(name, base, dict(sizes, bytes=need, q=ctypes.c_void_p(where), out=ctypes.c_void_p(where))) == xp.XP_ERR_SHAPE
+
+
+# ------------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("kv,heads,dim", [(1, 1, 64), (2, 8, 128), (8, 32, 128), (8, 40, 128), (4, 80, 64), (16, 16, 256), (1024, 1024, 64)])
+def test_one_workspace_for_every_step(kv, heads, dim):
+    """The packed tokens' workspace never falls as a step grows; chosen blocks' stays below the size that xp.h names."""
+    d = xp.kv_dims(kv, dim, 64, 4)
+    rows, batches, lens = (1, 2, 3, 4, 5, 8, 9, 15, 33, 64, 65, 100, 300, 2000), (1, 2, 7, 30, 64, 65, 300), (0, 1, 64, 512, 513, 1024, 1025, 2048, 2049, 70000)
+    size = {x: xp.xp_attn_chunk_workspace_bytes(d, heads, *x) for x in itertools.product(rows, batches, lens)}
+    for i, axis in enumerate((rows, batches, lens)):
+        for x in size:
+            at = axis.index(x[i]) + 1
+            if at < len(axis):
+                assert 16 <= size[x] <= size[x[:i] + (axis[at],) + x[i + 1:]], x
+    # 512 pieces of a block's rows (128 at 256 columns) and as many of sixteens: outputs, maxima, sums and factors
+    # in fp32; the list of 256 cut units before them, 28 bytes each, to whole 256
+    cut = 512 * ((128 if dim == 256 else 256) + 16) * (dim + 3) * 4 + 7424
+    assert set(size.values()) == {16, cut} and round(cut / 1e6) == {64: 37, 128: 73, 256: 76}[dim]
+    most = 1024 * (16 * dim + 48)
+    for n in list(range(1, 40)) + [63, 64, 100, 127, 128, 129, 255, 256, 257, 2000]:
+        for keep in list(range(1, 80)) + [100, 255, 256, 1000, 4097, 16384, 1 << 24]:
+            assert 16 <= xp.xp_attn_sparse_workspace_bytes(d, heads, n, keep) <= most, (n, keep)
