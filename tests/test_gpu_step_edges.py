@@ -1,4 +1,5 @@
-"""GPU: a serving step's calls at their edges — an empty batch, one workspace for steps of any size."""
+"""GPU: a serving step's calls at their edges — an empty batch, sequences of more than one round
+of the plan with long runs of pages, a thousand sequences' attention, one workspace for steps of any size."""
 import numpy as np
 import pytest
 import torch
@@ -48,7 +49,32 @@ def test_plan_without_sequences_captured():
         assert cu.tolist() == [0] and seq.tolist() == [-1] * 9 and pos.tolist() == [-1] * 9 and slot.tolist() == [-1] * 9
 
 
+# ---------------------------------------- more than a round of sequences, long runs of pages
+@pytest.mark.parametrize("batch,cols,page,longest,rows,spare", [
+    (1100, 24, 64, 700, 400000, 1.0),       # all are served
+    (1100, 24, 64, 700, 400000, 0.97),      # the pool ends among those of the second round
+    (1100, 24, 64, 700, 212000, 1.0),       # the rows end there
+    (2100, 24, 64, 700, 10 ** 6, 1.0), (2100, 24, 64, 700, 10 ** 6, 0.7), (1025, 12, 128, 700, 400000, 1.0)])
+def test_plan_and_release_of_many_sequences_with_long_runs(batch, cols, page, longest, rows, spare):
+    base.test_plan_and_release(batch, cols, page, longest, rows, spare)
+
+
 # ---------------------------------------------------------------------- attention
+def test_chunk_of_a_thousand_sequences():
+    """Single tokens beside a piece and a long context, which is cut."""
+    rng = np.random.default_rng(1000)
+    batch, kv, group, dim = 1000, 1, 4, 64
+    counts, start = np.ones(batch, dtype=np.int64), rng.integers(0, 200, batch)
+    counts[::50], counts[700], start[700], start[999] = 0, 300, 100, 9000
+    c = filled(rng, kv, dim, 64, 300)
+    table = rng.integers(0, 300, (batch, 142)).astype(np.int32)      # pages shared: the call only reads them
+    cu = ends(counts)
+    q = base.some_q(rng, int(cu[-1]) + 1, kv * group, dim, "bf16")
+    out = base.run_chunk(c, on_device(c), table, cu, start, q, 0.125)
+    assert (out[-1] == 3.0).all()
+    base.check_chunk(c, table, cu, start, q, out, 0.125)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_one_workspace_for_steps_of_any_size(dim):
     """Chosen blocks over the size that suits every call, packed tokens over the largest step's: the bits of calls with their own."""
