@@ -14,8 +14,8 @@
 // ones; the maximum may lag by 2^2 (see xp_attn_prompt.hip). Sixteens are as decode attention.
 //
 // Few rows of a sequence (single tokens, what is left behind whole blocks) would leave most of
-// a workgroup's waves idle: they are taken 16 at a time by decode attention's steps, every wave
-// its own tiles from registers, and the waves join at the end.
+// a workgroup's waves idle: they are taken 16 at a time as decode attention takes its rows (by the
+// steps of xp_attn_dev.h), every wave its own tiles from registers, and the waves join at the end.
 //
 // A batch is shared out on the device, from its lengths: every (block of rows or sixteen of
 // rows, kv head) is a unit, and units with more tiles than an even share of the whole are cut
@@ -26,6 +26,11 @@
 // exponentials wait for the scores and the second product for them: 988 TFLOP/s, 2,048 rows of
 // 32 heads of 128 behind 16,384 positions in 591 us. A mixed step of 512 rows and 16 single tokens
 // behind up to 4,000 positions takes 67 us.
+//
+// Every workgroup forms the table of pieces for itself, 64 sequences a step and up to three times over
+// the batch, before its first tile: little for tens of sequences, most of the time for many. 255
+// single tokens behind up to 300 positions take 87 us and 1,000 of them 762 (32 heads of 128, 8 kv
+// heads; their bytes take 11 and 42), behind up to 2,000 positions 159 and 1,199 (66 and 260).
 #include "xp_attn_dev.h"
 
 namespace xp {
@@ -180,7 +185,13 @@ __device__ __forceinline__ Cut cut_of(int tiles, float limit) {
 // A join takes 9 us by itself, whence the shortest pieces.
 constexpr float kLeast[2] = {8.0f, 16.0f};
 constexpr float kFixed = 16.0f, kJoin = 0.15f;
-constexpr int kSought = 64;        // sequences up to which the best of 16 lengths is sought
+// Up to so many sequences (a lane each) the best of 16 lengths is sought, beyond that pieces are an even
+// share. Searched and even, 32 heads of 128: 512 rows and 15 single tokens behind up to 4,000 positions
+// 77 and 86 us (in a graph), four pieces of up to 300 rows 77 and 100, 33 rows behind 65,000 69 and 86,
+// 512 rows and 16 single tokens behind up to 30,000 347 and 418. Single tokens alone lose by it, the more
+// of them: 8 behind up to 4,000 21 and 20, 32 47 and 41, 63 68 and 51; with a piece of 512 rows from some
+// 24 on: 24 90 and 85, 32 86 and 87, 63 130 and 104: the estimate leaves their pieces longer than an even share.
+constexpr int kSought = 64;
 struct Limits {
     float tiles[2];
 };

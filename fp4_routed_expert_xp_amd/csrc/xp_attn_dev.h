@@ -1,7 +1,9 @@
-// xp_attn_dev.h — a wave's view of one tile of the 4-bit cache for 16 query rows, as decode
-// attention (xp_attn.hip), attention over chosen blocks (xp_attn_sparse.hip) and the few rows
-// of a sequence in a mixed step (xp_attn_chunk.hip) have it. Lane (c, q) = (lane % 16,
-// lane / 16); see xp_attn.hip for the order of positions and the precision.
+// xp_attn_dev.h — a wave's view of one tile of the 4-bit cache for 16 query rows. Decode attention
+// (xp_attn.hip) takes the keys, their decoding and the rounding of outputs from here, and has steps
+// for values, softmax and joins of its own, for one or two sixteens of rows; attention over chosen
+// blocks (xp_attn_sparse.hip) and the few rows of a sequence in a mixed step (xp_attn_chunk.hip)
+// share all of it. Lane (c, q) = (lane % 16, lane / 16); order of positions and precision are
+// decode's: see xp_attn.hip.
 #pragma once
 
 #include "xp_kv_dev.h"

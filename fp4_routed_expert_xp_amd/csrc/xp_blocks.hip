@@ -339,7 +339,7 @@ __device__ __forceinline__ int blocks_of(const Select& a, int row, int b) {
 // there are just as many the rest of its bits does not matter.
 // Up to 64 kept, few lanes' largest keys tell which keys are worth it: as many lanes as are kept have
 // one at or above some bound, so the last one kept is not below it. What is at or above it is most often
-// a wave's worth, a key a lane, in `few` (512 rows of 16 blocks of 1,016: 31 us without, 28 with).
+// a wave's worth, a key a lane, in `few` (512 rows of 16 blocks of 1,016: 31.2 us without, 26.5 with).
 struct Few {
     uint32_t key;
     int block;
@@ -471,8 +471,9 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void select_kernel(Select a)
 
 // A row and a kv head a workgroup, any number of blocks: the key of the last block kept by
 // counting passes of 8 bits over LDS; then each wave walks its run of blocks, once to count
-// and once to write. (One wave that lists a row from registers, as above, takes 12.8 us where
-// this takes 9.2: 30 rows of 8 kv heads over 516 blocks.)
+// and once to write. (Rows alone through the kernel above, listed by one wave from registers, take
+// 12.5 us where this takes 9.8: 30 rows of 8 kv heads over up to 516 blocks, in a graph. Over up to
+// 1,564 they take 23.7 and 16.1; 10 rows over up to 316 10.8 and 8.2.)
 template <int D, bool BF16>
 __global__ __launch_bounds__(1024) void select_row_kernel(Select a) {
     extern __shared__ uint32_t keys[];
@@ -579,9 +580,18 @@ template <int D, bool BF16>
 static int launch(Select a, int most, hipStream_t s) {
     const long long pairs = (long long)a.m.rows * a.g.kv_heads;
     // Rows of a sequence share a workgroup where they are neighbours on average and there are more than
-    // three for each CU, or one where blocks are many (8 kv heads; 1,016 blocks: 32 rows 13.9 us, one by
-    // one 12.2; 48 rows 13.8 and 21.7; 512 rows 27 and 68. 313 blocks: 64 rows 10.5 and 10.1, 128 rows 10.7
-    // and 12.4. 47 blocks: 64 rows 8.6 and 7.3, 128 rows 8.7 and 9.0, 256 rows 10.4 and 13.4).
+    // three for each CU, or one where blocks are many. 8 kv heads, us shared and one by one:
+    //   4 heads of each: 47 blocks 64 rows 8.6 and 7.3, 128 rows 8.7 and 9.0, 256 rows 10.4 and 13.4; 316
+    //   blocks 64 rows 11.1 and 10.7, 90 11.1 and 11.9, 128 11.3 and 13.2; 520 blocks 36 rows 12.7 and 11.8,
+    //   64 12.8 and 13.0, 128 13.2 and 17.6; 816 blocks 36 rows 13.6 and 14.3, 64 13.9 and 16.0; 1,020 blocks
+    //   36 rows 14.2 and 15.8, 128 14.7 and 24.7; 512 rows 27 and 68.
+    // One, two and eight heads pay more for sharing, so that the rule takes the slower side for up to 64 rows
+    // between 512 and 816 blocks and, of eight heads, for 90: 520 blocks 36 rows of two 14.3 and 11.9, 64 14.4
+    // and 13.0, 90 14.7 and 15.2, 90 of eight 17.2 and 15.5; 816 blocks 36 rows of two 15.7 and 14.3, 64 16.2
+    // and 15.8; 1,020 blocks 36 rows of two 16.0 and 15.7, of eight 15.9 and 15.9.
+    // Groups of other sizes (3, 5, 6, 7, more than 8) are always one by one: 512 rows over 1,016 blocks take
+    // 74 us of five and 71 of seven heads, 51 of eight. `most` is the table's: one of more than kShort
+    // blocks has all rows one by one, and LDS for every block, however short its sequences are.
     const bool many = most <= kShort && (a.group == 1 || a.group == 2 || a.group == 4 || a.group == 8) &&
                       a.m.rows >= 4ll * a.m.batch && pairs > (most > 512 ? 1 : 3) * kCus;
     a.together = !many ? 1 : (a.group == 8 ? 2 : 4);
